@@ -184,6 +184,10 @@ typedef struct muonh_opts {
                                    supported (anything else: MUONH_EINVAL) */
   int          deterministic;   /* 1 (default) or 0.  Every reduction is two-stage and bitwise
                                    reproducible either way; 0 selects no faster path */
+  const float* grad_scale;      /* device, one float, read by the queued kernels: muonh_step and
+                                   adamh_step use grad_scale[0] * G in place of G (not rounded to
+                                   state_dtype), e.g. muonh_grad_norm's clipping coefficient;
+                                   NULL (default): G itself.  Not used by the other entry points */
 } muonh_opts;
 
 /* Fill *o with the defaults listed above. */
@@ -311,6 +315,84 @@ int ns_orthogonalize(const void* const in[], void* const out[], const int64_t sh
  */
 int frob_project(void* const W[], const void* const U[], const int64_t shapes[], int n,
                  float eta, const float rho[], const muonh_opts* opts);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the step: the gradients it consumes.
+ *
+ * The entry points below hold no state: scratch memory comes from the caller
+ * (device memory, 256-byte aligned, of at least the size the matching
+ * ..._workspace function gives; its content before and after the call means
+ * nothing, and it is free for other use once the call's work has run on
+ * `stream`).  So calls on different streams, threads and devices are
+ * independent as long as their buffers are, nothing is allocated, and every
+ * call can be captured into a graph, also as the first one.  `stream` is a
+ * hipStream_t of the current device (NULL: the null stream) and no call waits
+ * for the device.  Arguments are validated before any work is queued
+ * (MUONH_EINVAL; MUONH_ENOMEM: the workspace is too small).  All sums have a
+ * fixed order: results are bitwise reproducible.
+ * ---------------------------------------------------------------------------
+ *
+ * muonh_grad_norm -- the 2-norm over all gradients of a model together, and
+ * the coefficient that clips it:
+ *   norms[t] = ||g_t||,  total = sqrt(sum_t ||g_t||^2),
+ *   coef     = min(1, max_norm / (total + 1e-6))
+ * Pass coef as opts->grad_scale and muonh_step / adamh_step work on the
+ * clipped gradients with no further pass over them.
+ *   grads[t]   device, numel[t] elements of dtypes[t] (MUONH_F32 / MUONH_BF16),
+ *              contiguous, aligned to the element; may be NULL if numel[t] = 0
+ *   numel      host, n int64, >= 0;  dtypes  host, n ints;  n >= 1
+ *   max_norm   finite, >= 0; ignored when coef is NULL
+ *   total      device, 1 float
+ *   coef       device, 1 float, or NULL
+ *   norms      device, n floats, or NULL
+ * Squares are summed in fp64.  A NaN anywhere makes total and coef NaN; an
+ * infinity makes total infinite and coef 0.
+ */
+size_t muonh_grad_norm_workspace(int n);
+int muonh_grad_norm(const void* const grads[], const int64_t numel[], const int dtypes[], int n, float max_norm,
+                    float* total, float* coef, float* norms, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * muonh_clip_grads -- muonh_grad_norm, then outs[t] = coef * grads[t] in the
+ * gradient's own dtype (one rounding).  outs[t] may be grads[t] (in place;
+ * nothing is written when coef is 1), else the buffers must not overlap.
+ * Workspace: muonh_grad_norm_workspace(n).
+ */
+int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_t numel[], const int dtypes[], int n,
+                     float max_norm, float* total, float* coef, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * muonh_embedding -- out[i] = scale * table[id_i] for n tokens; a row of zeros
+ * for an id outside [0, rows) (padding).
+ *   table   device, rows x width, MUONH_F32 (master weights) or MUONH_BF16
+ *   ids     device, n integers of id_bits (32 or 64), signed
+ *   out     device, n x width, MUONH_F32 or MUONH_BF16 (one rounding)
+ *   n       0 .. 2^31 - 1;  rows  1 .. 2^31 - 2;  width  1 .. 2^18 (larger:
+ *           MUONH_ENOTIMPL);  scale  finite
+ * Rows whose width is a multiple of 8, on 16-byte aligned buffers, take
+ * 16-byte accesses; others are read element by element.
+ */
+int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t width, const void* ids, int id_bits,
+                    int64_t n, float scale, void* out, int out_dtype, void* stream);
+
+/*
+ * muonh_embedding_grad -- the gradient of muonh_embedding's table:
+ *   dtable[v] = scale * sum over the tokens i with id_i = v of dout[i]
+ * summed in fp32 and rounded once; rows without a token become zero, tokens
+ * with ids outside [0, rows) are left out.  accumulate = 1 adds to dtable
+ * instead (rows without a token stay as they are), e.g. to the output layer's
+ * gradient of a tied table.  The tokens are sorted by id in the call, so each
+ * row is a sum in a fixed order.
+ *   dout    device, n x width, MUONH_F32 or MUONH_BF16
+ *   dtable  device, rows x width, MUONH_F32 or MUONH_BF16, must not overlap dout
+ * Other arguments as muonh_embedding; n = 0 clears dtable (or leaves it).
+ */
+size_t muonh_embedding_grad_workspace(int64_t n, int64_t rows, int64_t width);
+int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* dout, int dout_dtype, float scale,
+                         int accumulate, void* dtable, int dtable_dtype, int64_t rows, int64_t width, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /*
  * Device flag counters, accumulated since the last reset:

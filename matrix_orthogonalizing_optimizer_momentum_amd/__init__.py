@@ -23,7 +23,15 @@ Entry points mirror the C ABI in ``include/muonh.h``:
 ``outward``, ``inward``, ``rb_eps``, ``workspace_limit`` (bytes),
 ``momentum`` ("sum" | "ema"), ``nesterov`` (bool), ``weight_decay`` (for
 hook "none"), ``lanes`` (concurrent lanes 1..4; 0: library default),
-``stream`` (a torch.cuda.Stream; default: the current stream).
+``stream`` (a torch.cuda.Stream; default: the current stream), ``grad_scale``
+(one float32 on the GPU that multiplies the gradients of ``muonh_step`` and
+``adamh_step``, such as the coefficient ``grad_norm`` returns).
+
+Around the step (``gradients.py``):
+
+* ``grad_norm(grads, max_norm=None)``, ``clip_grads(grads, max_norm, outputs=None)``
+* ``embedding(table, ids, scale=1.0, out=None, out_dtype=None)``,
+  ``embedding_grad(ids, dout, rows, scale=1.0, out=None, out_dtype=None, accumulate=False)``
 """
 from __future__ import annotations
 
@@ -44,6 +52,8 @@ EXPORTED = (
     "muonh_default_opts", "muonh_step", "muonh_step_noalloc", "adamh_step", "ns_orthogonalize", "frob_project", "muonh_get_flags",
     "muonh_reset_flags", "muonh_strerror", "muonh_release", "muonh_plan_query",
     "muonh_profile_begin", "muonh_profile_read", "muonh_version", "muonh_last_error",
+    "muonh_grad_norm_workspace", "muonh_grad_norm", "muonh_clip_grads",
+    "muonh_embedding", "muonh_embedding_grad_workspace", "muonh_embedding_grad",
 )
 
 
@@ -82,6 +92,7 @@ class Opts(ctypes.Structure):
         ("tile_sizes", POINTER(c_int)),
         ("param_dtype", c_int),
         ("deterministic", c_int),
+        ("grad_scale", c_void_p),
     ]
 
 
@@ -151,6 +162,22 @@ def load(path: str = LIB_PATH):
     lib.muonh_version.restype = ctypes.c_char_p
     lib.muonh_last_error.argtypes = []
     lib.muonh_last_error.restype = ctypes.c_char_p
+    lib.muonh_grad_norm_workspace.argtypes = [c_int]
+    lib.muonh_grad_norm_workspace.restype = c_size_t
+    lib.muonh_grad_norm.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_float, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_size_t, c_void_p]
+    lib.muonh_grad_norm.restype = c_int
+    lib.muonh_clip_grads.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_float, c_void_p, c_void_p,
+                                     c_void_p, c_size_t, c_void_p]
+    lib.muonh_clip_grads.restype = c_int
+    lib.muonh_embedding.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int, c_int64, c_float, c_void_p,
+                                    c_int, c_void_p]
+    lib.muonh_embedding.restype = c_int
+    lib.muonh_embedding_grad_workspace.argtypes = [c_int64, c_int64, c_int64]
+    lib.muonh_embedding_grad_workspace.restype = c_size_t
+    lib.muonh_embedding_grad.argtypes = [c_void_p, c_int, c_int64, c_void_p, c_int, c_float, c_int, c_void_p, c_int,
+                                         c_int64, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.muonh_embedding_grad.restype = c_int
     _LIB = lib
     return lib
 
@@ -198,7 +225,7 @@ def _dtype_code(t) -> int:
 def make_opts(state_dtype=MUONH_BF16, ns_dtype="bf16", ns_precision="h16", coeffs=None, ns_eps=None,
               zero_rel_eps=None, hook="hyperball", outward=None, inward=None, rb_eps=None,
               workspace_limit=0, stream=None, K=None, momentum="sum", nesterov=False, weight_decay=None, lanes=0,
-              hyperball_step="unit", tile_sizes=None):
+              hyperball_step="unit", tile_sizes=None, grad_scale=None):
     """Build an Opts struct; returns (opts, keepalive) where keepalive holds
     buffers the struct points to."""
     lib = load()
@@ -238,6 +265,12 @@ def make_opts(state_dtype=MUONH_BF16, ns_dtype="bf16", ns_precision="h16", coeff
     if rb_eps is not None:
         o.rb_eps = rb_eps
     o.workspace_limit = int(workspace_limit)
+    if grad_scale is not None:
+        import torch
+        if not grad_scale.is_cuda or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
+            raise ValueError("grad_scale must be one float32 on the GPU")
+        keep.append(grad_scale)
+        o.grad_scale = c_void_p(grad_scale.data_ptr())
     if stream is None:
         import torch
         stream = torch.cuda.current_stream()
@@ -422,12 +455,15 @@ def profile_begin():
 def profile_read():
     """{kernel class: dict(launches, total_ms, avg_ms, flops, bytes)} since profile_begin()."""
     lib = load()
-    buf = (KernelStat * 16)()
+    buf = (KernelStat * 32)()
     n = c_int(0)
-    _check(lib.muonh_profile_read(buf, 16, ctypes.byref(n)), "muonh_profile_read")
+    _check(lib.muonh_profile_read(buf, 32, ctypes.byref(n)), "muonh_profile_read")
     out = {}
     for i in range(n.value):
         s = buf[i]
         out[s.name.decode()] = dict(launches=int(s.launches), total_ms=s.total_ms,
                                     avg_ms=s.total_ms / max(1, s.launches), flops=s.flops, bytes=s.bytes)
     return out
+
+
+from .gradients import clip_grads, embedding, embedding_grad, grad_norm  # noqa: E402,F401

@@ -6,6 +6,7 @@
 //   k_hook_reduce, k_hook_write          (Hyperball or RadialBrake)
 // all queued on the caller's stream with no host synchronization.
 #include <hip/hip_runtime.h>
+#include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -19,6 +20,7 @@
 #include "muonh.h"
 #include "desc.h"
 #include "planner.h"
+#include "runtime.h"
 
 // Device memory the library holds without allocating it: the flag counters of
 // every entry point, and the scratch of muonh_step_noalloc (its workspace,
@@ -34,7 +36,7 @@ namespace muonh {
 // launchers (kernels_*.hip)
 hipError_t launch_momentum_prep(int state_dt, int op_dt, const MomMat* mats, const MomBlock* blocks,
                                 int nblocks, const NsUnit* units, const SlotTable& st, float beta,
-                                float gcoef, int nesterov, hipStream_t s);
+                                float gcoef, const float* gscale, int nesterov, hipStream_t s);
 hipError_t launch_hook_reduce(int mode, const HookMat* mats, const HookBlock* blocks, int nblocks,
                               const SlotTable& st, float eta, hipStream_t s);
 hipError_t launch_hook_write(int mode, const HookMat* mats, const HookBlock* blocks, int nblocks,
@@ -53,6 +55,21 @@ hipError_t launch_ns_gemm(int op_dt, int out_dt, int phase, int cfg, const NsUni
                           int no_mma, int master32, int seed32, const SlotTable& st, hipStream_t s);
 hipError_t launch_tile_ns(int state_dt, int op_dt, const TileMat* mats, const TileJob* jobs, int njobs,
                           const TileArgs& args, hipStream_t s);
+
+// Last HIP failure, for muonh_last_error().
+static thread_local char g_last_error[256] = "";
+
+int hip_fail(hipError_t e, const char* what) {
+  snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
+  return MUONH_EHIP;
+}
+
+void set_error(const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+}
 
 namespace {
 
@@ -142,8 +159,10 @@ State& S() {
 
 const char* kClassNames[] = {"momentum_prep", "ns_gram_G1", "ns_poly_G2",       "ns_update_G3",
                              "hook_reduce",   "hook_write", "sumsq",            "finalize",
-                             "ns_tile_resident", "adam_moments", "adam_write", "ns_tile_fused"};
-enum { PC_MOM = 0, PC_G1, PC_G2, PC_G3, PC_HR, PC_HW, PC_SQ, PC_FIN, PC_TILE, PC_AM, PC_AW, PC_T256, PC_N };
+                             "ns_tile_resident", "adam_moments", "adam_write", "ns_tile_fused",
+                             "grad_sumsq",    "grad_scale", "embedding",        "embedding_sort",
+                             "embedding_grad", "xent_prepare", "xent_logits",   "xent_prob", "xent_grad"};
+static_assert(sizeof(kClassNames) / sizeof(kClassNames[0]) == PC_N, "one name per kernel class");
 
 // ------------------------------------------------------------------ helpers
 // Frees a plan's device tables.  With a stream, stream-ordered allocations
@@ -545,20 +564,6 @@ SlotTable slot_table(const Meta& m, const DevTables& d) {
   return t;
 }
 
-// Last HIP failure, for muonh_last_error().
-thread_local char g_last_error[256] = "";
-
-int hip_fail(hipError_t e, const char* what) {
-  snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
-  return MUONH_EHIP;
-}
-
-#define MUONH_TRY_HIP(x)                                  \
-  do {                                                    \
-    const hipError_t e_ = (x);                            \
-    if (e_ != hipSuccess) return hip_fail(e_, #x);        \
-  } while (0)
-
 // Device addresses of the static symbols on one GPU, looked up once per
 // device with that device current.
 constexpr int kMaxDevices = 64;
@@ -675,6 +680,7 @@ int run_chunk_stage(State& st, const Meta& meta, int kind, const Cfg& cfg, const
         ta.gcoef = (kind == CALL_STEP && r.o.momentum_ema) ? 1.f - beta : 1.f;
         ta.nesterov = (kind == CALL_STEP && r.o.nesterov) ? 1 : 0;
         ta.eps = r.o.ns_eps;
+        ta.gscale = kind == CALL_STEP ? r.o.grad_scale : nullptr;
         ta.st = sl;
         for (const TileGroup& g : d.tile_groups) {
           ta.T = g.T;
@@ -697,7 +703,7 @@ int run_chunk_stage(State& st, const Meta& meta, int kind, const Cfg& cfg, const
           const bool stp = kind == CALL_STEP;
           MUONH_TRY_HIP(launch_momentum_prep(cfg.state_dt, cfg.op_dt, d.mom_mats, d.mom_blocks, d.n_mom, d.units,
                                              sl, stp ? beta : 0.f, (stp && r.o.momentum_ema) ? 1.f - beta : 1.f,
-                                             (stp && r.o.nesterov) ? 1 : 0, s));
+                                             stp ? r.o.grad_scale : nullptr, (stp && r.o.nesterov) ? 1 : 0, s));
         }
         Prof pf(st, s, PC_FIN, 0, 0);
         MUONH_TRY_HIP(launch_finalize(sl, 0, d.nunits, s));  // ||M||^2 per unit
@@ -900,6 +906,29 @@ int validate_common(const int64_t* shapes, int n, int K, int tile_T) {
 }
 
 }  // namespace
+
+ProfScope::ProfScope(hipStream_t s, int cls, double flops, double bytes)
+    : s_(s), cls_(cls), flops_(flops), bytes_(bytes) {
+  State& st = S();
+  std::lock_guard<std::mutex> lk(st.mu);
+  if (!st.profiling) return;
+  if (hipEventCreate(&e0_) != hipSuccess) e0_ = nullptr;
+  if (e0_) (void)hipEventRecord(e0_, s_);
+}
+
+ProfScope::~ProfScope() {
+  if (!e0_) return;
+  hipEvent_t e1{};
+  if (hipEventCreate(&e1) != hipSuccess) {
+    (void)hipEventDestroy(e0_);
+    return;
+  }
+  (void)hipEventRecord(e1, s_);
+  State& st = S();
+  std::lock_guard<std::mutex> lk(st.mu);
+  st.prof.push_back({cls_, e0_, e1, flops_, bytes_});
+}
+
 }  // namespace muonh
 
 using namespace muonh;
@@ -929,6 +958,7 @@ void muonh_default_opts(muonh_opts* o) {
   o->tile_sizes = nullptr;
   o->param_dtype = MUONH_F32;
   o->deterministic = 1;
+  o->grad_scale = nullptr;
 }
 
 int muonh_step(void* const params[], const void* const grads[], void* const moms[], const int64_t shapes[],
@@ -1006,7 +1036,7 @@ int adamh_step(void* const params[], const void* const grads[], void* const exp_
   // bias corrections in double, from the step count
   const double bc1 = 1.0 - std::pow((double)beta1, (double)step), bc2 = 1.0 - std::pow((double)beta2, (double)step);
   if (!(bc1 > 0.0) || !(bc2 > 0.0)) return MUONH_EINVAL;
-  p.adam = AdamArgs{beta1, beta2, (float)(1.0 / bc1), (float)(1.0 / bc2), eps};
+  p.adam = AdamArgs{beta1, beta2, (float)(1.0 / bc1), (float)(1.0 / bc2), eps, r.o.grad_scale};
   return run_call(CALL_ADAM, shapes, n, 0, 0, r, p, 0.f);
 }
 

@@ -1,0 +1,246 @@
+// Entry points around the optimizer step: gradient norm and clipping, the
+// embedding and its gradient, the output layer's cross entropy.  They hold no
+// state: each call validates, computes its layout on the host and queues
+// kernels on the caller's stream, with scratch memory from the caller.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "desc.h"
+#include "embed.h"
+#include "grad.h"
+#include "muonh.h"
+#include "runtime.h"
+
+namespace muonh {
+namespace {
+
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// ------------------------------------------------------------ gradient norm
+// Blocks of all tensors together: about 8 for each of the 256 CUs (all
+// resident at once), at least kMinChunk elements each.
+constexpr int64_t kGradBlocks = 2048;
+constexpr int64_t kMinChunk = 8192;
+
+// Elements per block: with it the blocks of n tensors are at most
+// kGradBlocks + n.
+int64_t grad_chunk(int64_t total) {
+  return std::max(kMinChunk, up((total + kGradBlocks - 1) / kGradBlocks, 2048));
+}
+
+int check_grads(const void* const* grads, const int64_t* numel, const int* dtypes, int n, int64_t& total) {
+  if (!grads || !numel || !dtypes || n <= 0) return MUONH_EINVAL;
+  total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] < 0 || numel[i] > ((int64_t)1 << 46)) return MUONH_EINVAL;
+    if (dtypes[i] != MUONH_F32 && dtypes[i] != MUONH_BF16) return MUONH_EINVAL;
+    if (numel[i] > 0 && !grads[i]) return MUONH_EINVAL;
+    if (numel[i] > 0 && (uintptr_t)grads[i] % (dtypes[i] == MUONH_F32 ? 4 : 2) != 0) return MUONH_EINVAL;
+    total += numel[i];
+  }
+  return total > ((int64_t)1 << 50) ? MUONH_EINVAL : MUONH_OK;
+}
+
+// The table of tensors [i0, i0 + t.n) and its number of blocks.
+int fill_table(GradTab& t, const void* const* grads, const int64_t* numel, const int* dtypes, int i0, int n,
+               int64_t chunk) {
+  t.n = std::min(n - i0, kTabTensors);
+  t.tensor0 = i0;
+  t.chunk = chunk;
+  std::fill(t.bf16, t.bf16 + kTabTensors / 32, 0u);
+  int64_t b = 0;
+  for (int k = 0; k < t.n; ++k) {
+    t.in[k] = grads[i0 + k];
+    t.numel[k] = numel[i0 + k];
+    t.first[k] = (int32_t)b;
+    if (dtypes[i0 + k] == MUONH_BF16) t.bf16[k / 32] |= 1u << (k % 32);
+    b += std::max<int64_t>(1, (numel[i0 + k] + chunk - 1) / chunk);
+  }
+  return (int)b;
+}
+
+int queue_norm(const void* const* grads, const int64_t* numel, const int* dtypes, int n, int64_t total_elems,
+               float max_norm, float* total, float* coef, float* norms, void* ws, hipStream_t s) {
+  const int64_t chunk = grad_chunk(total_elems);
+  int32_t* const bounds = reinterpret_cast<int32_t*>(ws);
+  double* const partials = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + up(4 * (int64_t)n, 256));
+  double bytes = 0;
+  for (int i = 0; i < n; ++i) bytes += (double)numel[i] * (dtypes[i] == MUONH_BF16 ? 2 : 4);
+  ProfScope pf(s, PC_GNORM, 0, bytes);
+  int part = 0;
+  for (int i0 = 0; i0 < n; i0 += kTabTensors) {
+    GradTab t;
+    const int nb = fill_table(t, grads, numel, dtypes, i0, n, chunk);
+    t.part0 = part;
+    part += nb;
+    MUONH_TRY_HIP(launch_grad_sumsq(t, nb, partials, bounds, s));
+  }
+  MUONH_TRY_HIP(launch_grad_finish(partials, bounds, n, part, max_norm, total, coef, norms, s));
+  return MUONH_OK;
+}
+
+// ------------------------------------------------------------------ embedding
+bool bad_dtype(int d) { return d != MUONH_F32 && d != MUONH_BF16; }
+int64_t dtype_size(int d) { return d == MUONH_F32 ? 4 : 2; }
+int internal_dtype(int d) { return d == MUONH_F32 ? DT_F32 : DT_BF16; }
+bool misaligned(const void* p, int64_t a) { return (uintptr_t)p % a != 0; }
+
+// n tokens, a table of rows x width; n = 0 is allowed.
+int check_embedding(const void* ids, int id_bits, int64_t n, int64_t rows, int64_t width) {
+  if (n < 0 || n > INT32_MAX || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;
+  if (id_bits != 32 && id_bits != 64) return MUONH_EINVAL;
+  if (n > 0 && (!ids || misaligned(ids, id_bits / 8))) return MUONH_EINVAL;
+  return width > kEmbMaxWidth ? MUONH_ENOTIMPL : MUONH_OK;
+}
+
+// Scratch of the embedding gradient.
+struct EmbedPlan {
+  int bits, passes, tile, blocks;
+  int64_t key[2], pos[2], hist, part, bytes;
+};
+
+EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
+  EmbedPlan p{};
+  int need = 1;  // bits of the largest key, rows itself (the ignored tokens)
+  while (((int64_t)1 << need) <= rows) ++need;
+  p.passes = (need + kSortBits - 1) / kSortBits;
+  p.bits = (need + p.passes - 1) / p.passes;
+  // tiles of at least 1024 tokens (256 a wave), at most kSortMaxBlocks of them:
+  // every block reads the counts of all
+  p.tile = (int)std::max<int64_t>(1024, up((n + kSortMaxBlocks - 1) / kSortMaxBlocks, 256));
+  p.blocks = (int)((n + p.tile - 1) / p.tile);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  for (int k = 0; k < 2; ++k) {
+    p.key[k] = take(4 * n);
+    p.pos[k] = take(4 * n);
+  }
+  p.hist = take(4 * ((int64_t)p.blocks << p.bits));
+  p.part = take(8 * ((n + kRun - 1) / kRun) * width);
+  p.bytes = std::max<int64_t>(at, 256);
+  return p;
+}
+
+}  // namespace
+}  // namespace muonh
+
+using namespace muonh;
+
+extern "C" {
+
+size_t muonh_grad_norm_workspace(int n) {
+  if (n <= 0) return 0;
+  return (size_t)(up(4 * (int64_t)n, 256) + 8 * (kGradBlocks + (int64_t)n));
+}
+
+int muonh_grad_norm(const void* const grads[], const int64_t numel[], const int dtypes[], int n, float max_norm,
+                    float* total, float* coef, float* norms, void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t elems = 0;
+  const int rc = check_grads(grads, numel, dtypes, n, elems);
+  if (rc != MUONH_OK) return rc;
+  if (!total || !workspace || (uintptr_t)workspace % 256 != 0) return MUONH_EINVAL;
+  if (coef && (!std::isfinite(max_norm) || max_norm < 0.f)) return MUONH_EINVAL;
+  if (workspace_bytes < muonh_grad_norm_workspace(n)) return MUONH_ENOMEM;
+  return queue_norm(grads, numel, dtypes, n, elems, max_norm, total, coef, norms, workspace,
+                    reinterpret_cast<hipStream_t>(stream));
+}
+
+int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_t numel[], const int dtypes[], int n,
+                     float max_norm, float* total, float* coef, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int64_t elems = 0;
+  const int rc = check_grads(grads, numel, dtypes, n, elems);
+  if (rc != MUONH_OK) return rc;
+  if (!outs || !total || !coef || !workspace || (uintptr_t)workspace % 256 != 0) return MUONH_EINVAL;
+  for (int i = 0; i < n; ++i)
+    if (numel[i] > 0 && (!outs[i] || (uintptr_t)outs[i] % (dtypes[i] == MUONH_F32 ? 4 : 2) != 0)) return MUONH_EINVAL;
+  if (!std::isfinite(max_norm) || max_norm < 0.f) return MUONH_EINVAL;
+  if (workspace_bytes < muonh_grad_norm_workspace(n)) return MUONH_ENOMEM;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int rq = queue_norm(grads, numel, dtypes, n, elems, max_norm, total, coef, nullptr, workspace, s);
+  if (rq != MUONH_OK) return rq;
+  double bytes = 0;
+  for (int i = 0; i < n; ++i) bytes += 2.0 * (double)numel[i] * (dtypes[i] == MUONH_BF16 ? 2 : 4);
+  ProfScope pf(s, PC_GSCALE, 0, bytes);
+  const int64_t chunk = grad_chunk(elems);
+  for (int i0 = 0; i0 < n; i0 += kTabTensors) {
+    ScaleTab t;
+    const int nb = fill_table(t.g, grads, numel, dtypes, i0, n, chunk);
+    for (int k = 0; k < t.g.n; ++k) t.out[k] = outs[i0 + k];
+    MUONH_TRY_HIP(launch_grad_scale(t, nb, coef, s));
+  }
+  return MUONH_OK;
+}
+
+int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t width, const void* ids, int id_bits,
+                    int64_t n, float scale, void* out, int out_dtype, void* stream) {
+  int rc = check_embedding(ids, id_bits, n, rows, width);
+  if (rc != MUONH_OK) return rc;
+  if (bad_dtype(table_dtype) || bad_dtype(out_dtype) || !std::isfinite(scale)) return MUONH_EINVAL;
+  if (!table || misaligned(table, dtype_size(table_dtype))) return MUONH_EINVAL;
+  if (n > 0 && (!out || misaligned(out, dtype_size(out_dtype)))) return MUONH_EINVAL;
+  if (n == 0) return MUONH_OK;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  ProfScope pf(s, PC_EMB, 0, (double)n * (double)width * (double)(dtype_size(table_dtype) + dtype_size(out_dtype)));
+  const EmbedArgs a{table, ids, out, n, rows, width, scale, id_bits};
+  MUONH_TRY_HIP(launch_embedding(internal_dtype(table_dtype), internal_dtype(out_dtype), a, s));
+  return MUONH_OK;
+}
+
+size_t muonh_embedding_grad_workspace(int64_t n, int64_t rows, int64_t width) {
+  if (check_embedding(nullptr, 32, 0, rows, width) != MUONH_OK || n < 0 || n > INT32_MAX) return 0;
+  return (size_t)embed_plan(n, rows, width).bytes;
+}
+
+int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* dout, int dout_dtype, float scale,
+                         int accumulate, void* dtable, int dtable_dtype, int64_t rows, int64_t width, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int rc = check_embedding(ids, id_bits, n, rows, width);
+  if (rc != MUONH_OK) return rc;
+  if (bad_dtype(dout_dtype) || bad_dtype(dtable_dtype) || !std::isfinite(scale)) return MUONH_EINVAL;
+  if (accumulate != 0 && accumulate != 1) return MUONH_EINVAL;
+  if (!dtable || misaligned(dtable, dtype_size(dtable_dtype))) return MUONH_EINVAL;
+  if (n > 0 && (!dout || misaligned(dout, dtype_size(dout_dtype)))) return MUONH_EINVAL;
+  if (!workspace || misaligned(workspace, 256)) return MUONH_EINVAL;
+  const EmbedPlan p = embed_plan(n, rows, width);
+  if (workspace_bytes < (size_t)p.bytes) return MUONH_ENOMEM;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* const ws = reinterpret_cast<char*>(workspace);
+  auto u32 = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
+  int cur = 0;
+  if (n > 0) {
+    ProfScope pf(s, PC_EMBSORT, 0, (double)n * (id_bits / 8 + 16.0 * p.passes - 8.0));
+    for (int k = 0; k < p.passes; ++k) {
+      SortPass sp{};
+      sp.ids = k == 0 ? ids : nullptr;
+      sp.key_in = u32(p.key[cur]);
+      sp.pos_in = u32(p.pos[cur]);
+      sp.key_out = u32(p.key[cur ^ 1]);
+      sp.pos_out = u32(p.pos[cur ^ 1]);
+      sp.hist = u32(p.hist);
+      sp.n = n;
+      sp.rows = (uint32_t)rows;
+      sp.id_bits = id_bits;
+      sp.shift = k * p.bits;
+      sp.bits = p.bits;
+      sp.tile = p.tile;
+      sp.blocks = p.blocks;
+      MUONH_TRY_HIP(launch_sort_pass(sp, s));
+      cur ^= 1;
+    }
+  }
+  ProfScope pf(s, PC_EMBGRAD, 0,
+               (double)n * width * dtype_size(dout_dtype) + (double)rows * width * dtype_size(dtable_dtype));
+  const EmbedGradArgs a{u32(p.key[cur]), u32(p.pos[cur]), dout, dtable, reinterpret_cast<float*>(ws + p.part),
+                        n, rows, width, scale, accumulate};
+  MUONH_TRY_HIP(launch_embedding_grad(internal_dtype(dout_dtype), internal_dtype(dtable_dtype), a, s));
+  return MUONH_OK;
+}
+
+}  // extern "C"

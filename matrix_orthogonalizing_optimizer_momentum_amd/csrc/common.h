@@ -169,6 +169,13 @@ __device__ __forceinline__ float load_dyn(const void* p, int64_t i, int dtype) {
   return gmem(reinterpret_cast<const float*>(p))[i];
 }
 
+// The weight of G in a momentum update: coef, times the caller's device scale
+// when there is one (opts.grad_scale).  The same for every lane.
+__device__ __forceinline__ float grad_weight(float coef, const float* gscale) {
+  if (gscale == nullptr) return coef;
+  return coef * __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(gmem(gscale)[0])));
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);

@@ -139,6 +139,7 @@ struct TileArgs {
   float gcoef;              // weight of G in the buffer update: 1 (sum) or 1 - beta (EMA)
   int nesterov;             // 1: NS input is gcoef*G + beta*M (Nesterov blend)
   float eps;                // pre-scale eps
+  const float* gscale;      // device scale of G (gcoef is multiplied by it), or nullptr
   SlotTable st;
 };
 
@@ -150,9 +151,10 @@ constexpr int kModeRel = 3;   // RelativeUpdate (update scaled to ||W||)
 
 // Adam's step constants (AdamH): m <- b1 m + (1 - b1) g,
 // v <- b2 v + (1 - b2) g^2, U = (m * ibc1) / (sqrt(v * ibc2) + eps) with the
-// bias corrections ibc = 1 / (1 - b^t).
+// bias corrections ibc = 1 / (1 - b^t) and g = G, or *gscale * G.
 struct AdamArgs {
   float b1, b2, ibc1, ibc2, eps;
+  const float* gscale;  // device scale of G, or nullptr
 };
 
 // Elements per block of the flat hook / norm passes (256 threads x 32).

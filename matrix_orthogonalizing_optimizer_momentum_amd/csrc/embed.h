@@ -1,0 +1,52 @@
+// Layout and launchers of the embedding kernels, shared by the kernels and
+// the entry points.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muonh {
+
+constexpr int64_t kEmbMaxWidth = (int64_t)1 << 18;
+constexpr int kSortThreads = 256;
+constexpr int kSortBits = 11;      // digit bits of one sort pass, at most
+constexpr int kSortMaxBlocks = 64;
+constexpr int kRun = 32;           // sorted tokens per piece of the gradient
+
+// One stable counting pass of the token sort.
+struct SortPass {
+  const void* ids;          // first pass: the token ids (id_bits wide); else nullptr
+  const uint32_t* key_in;   // later passes
+  const uint32_t* pos_in;
+  uint32_t* key_out;
+  uint32_t* pos_out;
+  uint32_t* hist;           // [blocks][1 << bits]
+  int64_t n;
+  uint32_t rows;            // ids outside [0, rows) get the key rows
+  int32_t id_bits, shift, bits, tile, blocks;
+};
+
+struct EmbedArgs {
+  const void* table;
+  const void* ids;
+  void* out;
+  int64_t n, rows, width;
+  float scale;
+  int32_t id_bits;
+};
+
+struct EmbedGradArgs {
+  const uint32_t* key;      // sorted token ids, the ignored ones (= rows) last
+  const uint32_t* pos;      // and where each token stands in the batch
+  const void* dout;         // n x width
+  void* dtable;             // rows x width
+  float* part;              // [pieces][2][width]: head and tail sums of runs that cross pieces
+  int64_t n, rows, width;
+  float scale;
+  int32_t accumulate;
+};
+
+hipError_t launch_embedding(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t s);
+hipError_t launch_sort_pass(const SortPass& p, hipStream_t s);
+hipError_t launch_embedding_grad(int g_dt, int out_dt, const EmbedGradArgs& a, hipStream_t s);
+
+}  // namespace muonh

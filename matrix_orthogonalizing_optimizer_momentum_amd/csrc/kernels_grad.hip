@@ -1,0 +1,215 @@
+// Global gradient norm over many tensors, and clipping (gfx950).
+//
+//   total   = sqrt(sum_t sum_e g_t[e]^2),  norms[t] = sqrt(sum_e g_t[e]^2)
+//   coef    = min(1, max_norm / (total + 1e-6))
+//   out_t   = coef * g_t
+//
+// Both passes stream: the norm reads every gradient once, clipping reads it
+// again and writes it.  The list of tensors travels in the kernel arguments
+// (kTabTensors a launch), so a call uploads no table, keeps nothing between
+// calls and can be captured into a graph as it is.
+//
+// Work split: every tensor is cut into blocks of `chunk` elements, one for the
+// whole call and chosen so that the blocks of all tensors together fill the
+// chip about once; a block sums its squares in fp64 (squares of bf16 and fp32
+// values neither overflow nor underflow there, and no order of the values
+// changes the result by more than a few units of fp64's last place) and stores
+// one partial.  k_grad_finish adds the partials in a fixed order.
+#include "common.h"
+#include "grad.h"
+
+namespace muonh {
+
+namespace {
+
+// Index of the tensor that block b belongs to: the last t < n with
+// first[t] <= b.  One load per lane and a count instead of a dependent chain.
+__device__ __forceinline__ int tensor_of(const int32_t* first, int n, int b) {
+  int t = -1;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int k = 0; k < kTabTensors / 64; ++k) {
+    const int i = 64 * k + lane;
+    const bool below = i < n && first[i] <= b;
+    t += __popcll(__ballot(below));
+  }
+  return __builtin_amdgcn_readfirstlane(t);
+}
+
+// Elements before the first 16-byte boundary of p.
+template <typename T>
+__device__ __forceinline__ int head_of(const void* p) {
+  return (int)(((16 - (uintptr_t)p % 16) % 16) / sizeof(T));
+}
+
+constexpr int kVec = 8;  // elements a thread takes at a time
+constexpr int kDepth = 4;  // such groups in flight
+
+template <typename T>
+__device__ __forceinline__ double sumsq_block(const T* __restrict__ p, int64_t lo, int64_t hi) {
+  const int t = threadIdx.x;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  // [lo, v0) and [v1, hi) are at most 7 elements each
+  const int64_t v0 = min(lo + head_of<T>(p), hi);
+  const int64_t v1 = v0 + (hi - v0) / kVec * kVec;
+  auto one = [&](int64_t i) {
+    const double x = (double)St<T>::ld(p, i);
+    s[0] = fma(x, x, s[0]);
+  };
+  if (t < 7 && lo + t < v0) one(lo + t);
+  if (t >= 8 && t < 15 && v1 + (t - 8) < hi) one(v1 + (t - 8));
+  auto add = [&](const Raw8<T>& r) {
+    float v[8];
+    r.unpack(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k & 3] = fma((double)v[k], (double)v[k], s[k & 3]);
+  };
+  constexpr int64_t kStep = (int64_t)kGradThreads * kVec;
+  int64_t i = v0 + (int64_t)t * kVec;
+  for (; i + (kDepth - 1) * kStep < v1; i += kDepth * kStep) {
+    Raw8<T> r[kDepth];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) r[k].load(p, i + k * kStep);
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) add(r[k]);
+  }
+  for (; i < v1; i += kStep) {
+    Raw8<T> r;
+    r.load(p, i);
+    add(r);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__global__ __launch_bounds__(kGradThreads) void k_grad_sumsq(const GradTab tab, double* __restrict__ partials,
+                                                             int32_t* __restrict__ bounds) {
+  __shared__ double red[kGradThreads / 64];
+  const int b = blockIdx.x;
+  const int t = tensor_of(tab.first, tab.n, b);
+  const int64_t n = tab.numel[t];
+  const int64_t lo = (int64_t)(b - tab.first[t]) * tab.chunk;
+  const int64_t hi = min(n, lo + tab.chunk);
+  double s;
+  if ((tab.bf16[t >> 5] >> (t & 31)) & 1) s = sumsq_block(reinterpret_cast<const bf16_t*>(tab.in[t]), lo, hi);
+  else s = sumsq_block(reinterpret_cast<const float*>(tab.in[t]), lo, hi);
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < kGradThreads / 64; ++k) v += red[k];
+    gmem(partials)[tab.part0 + b] = v;
+    // where this tensor's partials begin, for k_grad_finish
+    if (lo == 0) gmem(bounds)[tab.tensor0 + t] = tab.part0 + b;
+  }
+}
+
+// One workgroup: wave w sums the partials of tensors w, w + 16, ... (each lane
+// a fixed stride of them), then the waves' totals are added in order.
+__global__ __launch_bounds__(1024) void k_grad_finish(const double* __restrict__ partials,
+                                                      const int32_t* __restrict__ bounds, int n, int nparts,
+                                                      float max_norm, float* __restrict__ total,
+                                                      float* __restrict__ coef, float* __restrict__ norms) {
+  constexpr int NW = 16;
+  __shared__ double red[NW];
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  double mine = 0.0;
+  for (int t = w; t < n; t += NW) {
+    const int p0 = gmem(bounds)[t], p1 = t + 1 < n ? gmem(bounds)[t + 1] : nparts;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    int p = p0 + l;
+    for (; p + 192 < p1; p += 256) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += gmem(partials)[p + 64 * k];
+    }
+    for (; p < p1; p += 64) s[0] += gmem(partials)[p];
+    const double v = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+    mine += v;
+    if (l == 0 && norms != nullptr) gmem(norms)[t] = (float)sqrt(v);
+  }
+  if (l == 0) red[w] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v += red[k];
+    const double tot = sqrt(v);
+    gmem(total)[0] = (float)tot;
+    if (coef != nullptr) {
+      const double c = (double)max_norm / (tot + 1e-6);
+      gmem(coef)[0] = c >= 1.0 ? 1.f : (float)c;  // a NaN norm stays NaN
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_block(const T* p, T* o, int64_t lo, int64_t hi, float c) {
+  const int t = threadIdx.x;
+  if (((uintptr_t)p ^ (uintptr_t)o) % 16 != 0) {  // no common 16-byte grid
+    for (int64_t i = lo + t; i < hi; i += kGradThreads) St<T>::st(o, i, c * St<T>::ld(p, i));
+    return;
+  }
+  const int64_t v0 = min(lo + head_of<T>(p), hi);
+  const int64_t v1 = v0 + (hi - v0) / kVec * kVec;
+  if (t < 7 && lo + t < v0) St<T>::st(o, lo + t, c * St<T>::ld(p, lo + t));
+  if (t >= 8 && t < 15 && v1 + (t - 8) < hi) St<T>::st(o, v1 + (t - 8), c * St<T>::ld(p, v1 + (t - 8)));
+  auto put = [&](const Raw8<T>& r, int64_t i) {
+    float v[8];
+    r.unpack(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= c;
+    store8(o, i, v);
+  };
+  constexpr int64_t kStep = (int64_t)kGradThreads * kVec;
+  int64_t i = v0 + (int64_t)t * kVec;
+  for (; i + (kDepth - 1) * kStep < v1; i += kDepth * kStep) {
+    Raw8<T> r[kDepth];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) r[k].load(p, i + k * kStep);
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) put(r[k], i + k * kStep);
+  }
+  for (; i < v1; i += kStep) {
+    Raw8<T> r;
+    r.load(p, i);
+    put(r, i);
+  }
+}
+
+__global__ __launch_bounds__(kGradThreads) void k_grad_scale(const ScaleTab tab, const float* __restrict__ coef) {
+  const int b = blockIdx.x;
+  const int t = tensor_of(tab.g.first, tab.g.n, b);
+  const float c = gmem(coef)[0];
+  const void* const in = tab.g.in[t];
+  void* const out = tab.out[t];
+  if (c == 1.f && in == out) return;  // nothing to change in place
+  const int64_t n = tab.g.numel[t];
+  const int64_t lo = (int64_t)(b - tab.g.first[t]) * tab.g.chunk;
+  const int64_t hi = min(n, lo + tab.g.chunk);
+  if ((tab.g.bf16[t >> 5] >> (t & 31)) & 1)
+    scale_block(reinterpret_cast<const bf16_t*>(in), reinterpret_cast<bf16_t*>(out), lo, hi, c);
+  else
+    scale_block(reinterpret_cast<const float*>(in), reinterpret_cast<float*>(out), lo, hi, c);
+}
+
+}  // namespace
+
+hipError_t launch_grad_sumsq(const GradTab& tab, int nblocks, double* partials, int32_t* bounds, hipStream_t s) {
+  hipLaunchKernelGGL(k_grad_sumsq, dim3(nblocks), dim3(kGradThreads), 0, s, tab, partials, bounds);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_finish(const double* partials, const int32_t* bounds, int n, int nparts, float max_norm,
+                              float* total, float* coef, float* norms, hipStream_t s) {
+  hipLaunchKernelGGL(k_grad_finish, dim3(1), dim3(1024), 0, s, partials, bounds, n, nparts, max_norm, total, coef,
+                     norms);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const ScaleTab& tab, int nblocks, const float* coef, hipStream_t s) {
+  hipLaunchKernelGGL(k_grad_scale, dim3(nblocks), dim3(kGradThreads), 0, s, tab, coef);
+  return hipGetLastError();
+}
+
+}  // namespace muonh

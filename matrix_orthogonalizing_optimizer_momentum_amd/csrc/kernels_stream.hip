@@ -32,7 +32,9 @@ static_assert(kHookBlockElems == kHookThreads * kHookPerThread, "hook block size
 template <typename ST, typename OT>
 __global__ __launch_bounds__(kMomThreads) void k_momentum_prep(
     const MomMat* __restrict__ mats, const MomBlock* __restrict__ blocks,
-    const NsUnit* __restrict__ units, SlotTable st, float beta, float gcoef, int nesterov) {
+    const NsUnit* __restrict__ units, SlotTable st, float beta, float gcoef0, const float* gscale,
+    int nesterov) {
+  const float gcoef = grad_weight(gcoef0, gscale);
   __shared__ float tile[64][65];
   const MomBlock blk = blocks[blockIdx.x];
   const MomMat mm = mats[blk.mat];
@@ -422,14 +424,15 @@ __global__ __launch_bounds__(kHookThreads) void k_adam_moments(
   const HookBlock hb = blocks[blockIdx.x];
   const HookMat hm = mats[hb.mat];
   const GT* const g = reinterpret_cast<const GT*>(hm.o);
-  const float c1 = 1.f - a.b1, c2 = 1.f - a.b2;
+  const float c1 = 1.f - a.b1, c2 = 1.f - a.b2, gs = grad_weight(1.f, a.gscale);
   double s_uu = 0.0, s_wu = 0.0, s_ww = 0.0;
   const int64_t base = (int64_t)hb.blk * kHookBlockElems;
   auto update = [&](float (&gv)[8], float (&m)[8], float (&v)[8], const float (&w)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      m[k] = fmaf(a.b1, m[k], c1 * gv[k]);
-      v[k] = fmaf(a.b2, v[k], c2 * (gv[k] * gv[k]));
+      const float gk = gs * gv[k];
+      m[k] = fmaf(a.b1, m[k], c1 * gk);
+      v[k] = fmaf(a.b2, v[k], c2 * (gk * gk));
       if (SUMS) {
         const double u = (double)adam_u(m[k], v[k], a), wd = (double)w[k];
         s_uu = fma(u, u, s_uu);
@@ -651,11 +654,12 @@ __global__ __launch_bounds__(256) void k_finalize(SlotTable st, int slot0) {
 // ---------------------------------------------------------------------------
 hipError_t launch_momentum_prep(int state_dt, int op_dt, const MomMat* mats, const MomBlock* blocks,
                                 int nblocks, const NsUnit* units, const SlotTable& st, float beta,
-                                float gcoef, int nesterov, hipStream_t s) {
+                                float gcoef, const float* gscale, int nesterov, hipStream_t s) {
   if (nblocks <= 0) return hipSuccess;
   dim3 grid(nblocks), block(kMomThreads);
 #define MUONH_MOM(ST, OT) \
-  hipLaunchKernelGGL((k_momentum_prep<ST, OT>), grid, block, 0, s, mats, blocks, units, st, beta, gcoef, nesterov)
+  hipLaunchKernelGGL((k_momentum_prep<ST, OT>), grid, block, 0, s, mats, blocks, units, st, beta, gcoef, gscale, \
+                     nesterov)
   if (state_dt == DT_BF16 && op_dt == DT_BF16) MUONH_MOM(bf16_t, bf16_t);
   else if (state_dt == DT_BF16 && op_dt == DT_F32) MUONH_MOM(bf16_t, float);
   else if (state_dt == DT_F32 && op_dt == DT_BF16) MUONH_MOM(float, bf16_t);

@@ -121,6 +121,7 @@ void k_tile_ns(const TileMat* __restrict__ mats, const TileJob* __restrict__ job
   const int64_t ldm = mt.W;
   const ST* tg = mt.g ? reinterpret_cast<const ST*>(mt.g) + r0 * ldm + c0 : nullptr;
   ST* tm = reinterpret_cast<ST*>(mt.m) + r0 * ldm + c0;
+  const float gcoef = grad_weight(args.gcoef, args.gscale);
 
   // ---- load phase: the tile in 8-element row chunks (thread t takes chunks
   // t, t + 256, ...: consecutive threads read consecutive 16-byte pieces),
@@ -155,11 +156,11 @@ void k_tile_ns(const TileMat* __restrict__ mats, const TileJob* __restrict__ job
         float gv[8];
         gr[c].unpack(gv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = St<ST>::round(fmaf(args.beta, x[e], args.gcoef * gv[e]));
+        for (int e = 0; e < 8; ++e) x[e] = St<ST>::round(fmaf(args.beta, x[e], gcoef * gv[e]));
         if (ok) store8(tm, (int64_t)row * ldm + col, x);
         if (args.nesterov) {  // NS input: the Nesterov blend of G and the updated buffer
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(args.beta, x[e], args.gcoef * gv[e]);
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(args.beta, x[e], gcoef * gv[e]);
         }
       }
 #pragma unroll
@@ -183,9 +184,9 @@ void k_tile_ns(const TileMat* __restrict__ mats, const TileJob* __restrict__ job
           x = St<ST>::ld(tm, o);
           if (tg) {
             const float gg = St<ST>::ld(tg, o);
-            x = St<ST>::round(fmaf(args.beta, x, args.gcoef * gg));
+            x = St<ST>::round(fmaf(args.beta, x, gcoef * gg));
             St<ST>::st(tm, o, x);
-            if (args.nesterov) x = fmaf(args.beta, x, args.gcoef * gg);
+            if (args.nesterov) x = fmaf(args.beta, x, gcoef * gg);
           }
         }
         sq = fmaf(x, x, sq);

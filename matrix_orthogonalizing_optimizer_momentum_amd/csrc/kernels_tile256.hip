@@ -144,6 +144,7 @@ __device__ __forceinline__ void tile256_one(char* const smem, const TileMat* __r
   const int64_t ldm = mt.W;
   const bf16_t* const tg = mt.g ? reinterpret_cast<const bf16_t*>(mt.g) + r0 * ldm + c0 : nullptr;
   bf16_t* const tm = reinterpret_cast<bf16_t*>(mt.m) + r0 * ldm + c0;
+  const float gcoef = grad_weight(args.gcoef, args.gscale);
 
   // ---- input: momentum on the tile (8-element row chunks, chunk t + 256 c
   // for thread t), M stored back, X0 staged row-major in the matrix region.
@@ -176,8 +177,8 @@ __device__ __forceinline__ void tile256_one(char* const smem, const TileMat* __r
           float x[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[2 * e] = St<bf16_t>::round(fmaf(args.beta, lo_bf(mraw[sl][k][e]), args.gcoef * lo_bf(graw[sl][k][e])));
-            x[2 * e + 1] = St<bf16_t>::round(fmaf(args.beta, hi_bf(mraw[sl][k][e]), args.gcoef * hi_bf(graw[sl][k][e])));
+            x[2 * e] = St<bf16_t>::round(fmaf(args.beta, lo_bf(mraw[sl][k][e]), gcoef * lo_bf(graw[sl][k][e])));
+            x[2 * e + 1] = St<bf16_t>::round(fmaf(args.beta, hi_bf(mraw[sl][k][e]), gcoef * hi_bf(graw[sl][k][e])));
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
@@ -205,7 +206,7 @@ __device__ __forceinline__ void tile256_one(char* const smem, const TileMat* __r
           const int64_t o = (int64_t)row * ldm + col + e;
           v = St<bf16_t>::ld(tm, o);
           if (tg) {
-            v = St<bf16_t>::round(fmaf(args.beta, v, args.gcoef * St<bf16_t>::ld(tg, o)));
+            v = St<bf16_t>::round(fmaf(args.beta, v, gcoef * St<bf16_t>::ld(tg, o)));
             St<bf16_t>::st(tm, o, v);
           }
         }

@@ -1,0 +1,218 @@
+"""The gradients an optimizer step consumes: their global norm and clipping, the
+embedding and its gradient.
+
+Argument marshalling only, like the rest of the binding: the work is queued on
+``stream`` (default: the current stream of the tensors' device) and never waits
+for the device.  Outputs and scratch memory are torch allocations made for the
+call on that stream, so calls on different streams share nothing and every
+call can be captured into a graph.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from array import array
+from ctypes import c_void_p
+
+import torch
+
+from . import MUONH_BF16, MUONH_F32, MuonhError, load
+
+_CODE = {torch.float32: MUONH_F32, torch.bfloat16: MUONH_BF16}
+
+
+@contextlib.contextmanager
+def _switched(dev, stream):
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if stream.device.index != dev:
+                raise ValueError("stream belongs to another device than the tensors")
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _on(dev, stream):
+    """Context in which allocations and launches go to ``stream`` on device
+    ``dev``; gives the raw stream."""
+    if stream is None and dev == torch.cuda.current_device():
+        return contextlib.nullcontext(torch.cuda.current_stream(dev).cuda_stream)
+    return _switched(dev, stream)
+
+
+def _check(rc, where):
+    if rc:
+        raise MuonhError(rc, where)
+
+
+def _table(ts, what):
+    """(pointers, sizes, dtype codes, device) of a list of gradients, checked."""
+    ptrs, sizes, codes = array("Q"), array("q"), array("i")
+    dev = -1
+    for t in ts:
+        code = _CODE.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{what}: unsupported dtype {t.dtype}: use torch.bfloat16 or torch.float32")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{what}: tensors must be on the GPU")
+            if dev >= 0:
+                raise ValueError(f"{what}: tensors must be on one device")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous")
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+        codes.append(code)
+    return ptrs, sizes, codes, dev
+
+
+def _addr(a):
+    return a.buffer_info()[0]
+
+
+def grad_norm(grads, max_norm=None, stream=None):
+    """2-norm of all gradients together.
+
+    ``grads``: float32 / bfloat16 tensors of any shapes (contiguous, one
+    device).  Returns ``(total, coef, norms)``, float32 on the device: the
+    global norm, the clipping coefficient ``min(1, max_norm / (total + 1e-6))``
+    (``None`` without ``max_norm``) and the norm of every tensor.  Pass ``coef``
+    to ``muonh_step`` / ``adamh_step`` as ``grad_scale`` to step on the clipped
+    gradients without another pass over them.
+    """
+    n = len(grads)
+    if n == 0:
+        raise ValueError("no gradients")
+    ptrs, sizes, codes, dev = _table(grads, "grads")
+    lib = load()
+    with _on(dev, stream) as raw:
+        ws_bytes = lib.muonh_grad_norm_workspace(n)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=grads[0].device)
+        out = torch.empty(n + 2, dtype=torch.float32, device=grads[0].device)
+        p = out.data_ptr()
+        rc = lib.muonh_grad_norm(_addr(ptrs), _addr(sizes), _addr(codes), n, 0.0 if max_norm is None else max_norm,
+                                 p, None if max_norm is None else p + 4, p + 8, ws.data_ptr(), ws_bytes, raw)
+    _check(rc, "muonh_grad_norm")
+    return out[0], None if max_norm is None else out[1], out[2:]
+
+
+def clip_grads(grads, max_norm, outputs=None, stream=None):
+    """Scale the gradients so that their global norm is at most ``max_norm``.
+
+    ``outputs[i] = coef * grads[i]`` with ``grad_norm``'s coefficient;
+    ``outputs=None`` scales ``grads`` in place.  Returns ``(total, coef)``.
+    """
+    n = len(grads)
+    if n == 0:
+        raise ValueError("no gradients")
+    ptrs, sizes, codes, dev = _table(grads, "grads")
+    outs = ptrs
+    if outputs is not None:
+        outs, osizes, ocodes, odev = _table(outputs, "outputs")
+        if osizes != sizes or ocodes != codes or odev != dev:
+            raise ValueError("outputs must match grads in size, dtype and device")
+    lib = load()
+    with _on(dev, stream) as raw:
+        ws_bytes = lib.muonh_grad_norm_workspace(n)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=grads[0].device)
+        out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+        p = out.data_ptr()
+        rc = lib.muonh_clip_grads(_addr(ptrs), _addr(outs), _addr(sizes), _addr(codes), n, max_norm, p, p + 4,
+                                  ws.data_ptr(), ws_bytes, raw)
+    _check(rc, "muonh_clip_grads")
+    return out[0], out[1]
+
+
+def _plain(t, what, dev=None):
+    """Checks one tensor: on the GPU (device ``dev`` if given), contiguous; returns its device."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} must be on the GPU")
+    if dev is not None and d != dev:
+        raise ValueError(f"{what} is on another device")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return d
+
+
+def _code(t, what):
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}: use torch.bfloat16 or torch.float32")
+    return code
+
+
+def _id_bits(t, what):
+    if t.dtype == torch.int64:
+        return 64
+    if t.dtype == torch.int32:
+        return 32
+    raise TypeError(f"{what}: unsupported dtype {t.dtype}: use torch.int64 or torch.int32")
+
+
+def embedding(table, ids, scale=1.0, out=None, out_dtype=None, stream=None):
+    """``out[i] = scale * table[ids[i]]``, zeros for an id outside the table.
+
+    ``table``: rows x width, float32 or bfloat16; ``ids``: int64 / int32 of any
+    shape; ``out``: ``ids.shape + (width,)`` in ``out_dtype`` (default: the
+    table's), allocated unless given.  Returns ``out``.
+    """
+    if table.dim() != 2:
+        raise ValueError("table must be a matrix (2-D)")
+    dev = _plain(table, "table")
+    _plain(ids, "ids", dev)
+    bits, code = _id_bits(ids, "ids"), _code(table, "table")
+    shape = (*ids.shape, table.shape[1])
+    lib = load()
+    with _on(dev, stream) as raw:
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype or table.dtype, device=table.device)
+        else:
+            _plain(out, "out", dev)
+            if tuple(out.shape) != shape or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError("out must have the shape of ids and the table's width, and out_dtype")
+        rc = lib.muonh_embedding(table.data_ptr(), code, table.shape[0], table.shape[1], ids.data_ptr(), bits,
+                                 ids.numel(), scale, out.data_ptr(), _code(out, "out"), raw)
+    _check(rc, "muonh_embedding")
+    return out
+
+
+def embedding_grad(ids, dout, rows=None, scale=1.0, out=None, out_dtype=None, accumulate=False, stream=None):
+    """Gradient of ``embedding``'s table: ``out[v] = scale * sum of dout[i] over ids[i] == v``.
+
+    ``dout``: ``ids.shape + (width,)``, float32 or bfloat16; ``out``: ``rows`` x
+    width in ``out_dtype`` (default: dout's), allocated unless given.  Rows
+    without a token become zero; with ``accumulate`` the sums are added to
+    ``out`` instead.  Tokens with ids outside the table are left out.  Returns
+    ``out``.
+    """
+    dev = _plain(dout, "dout")
+    _plain(ids, "ids", dev)
+    bits, code = _id_bits(ids, "ids"), _code(dout, "dout")
+    if tuple(dout.shape[:-1]) != tuple(ids.shape) or dout.dim() != ids.dim() + 1:
+        raise ValueError("dout must have the shape of ids and one more axis, the table's width")
+    if out is None:
+        if rows is None:
+            raise ValueError("embedding_grad needs rows or out")
+        if accumulate:
+            raise ValueError("accumulate needs out")
+    else:
+        _plain(out, "out", dev)
+        rows = out.shape[0] if rows is None else rows
+        if tuple(out.shape) != (rows, dout.shape[-1]) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must be rows x width, of out_dtype")
+    width = dout.shape[-1]
+    lib = load()
+    with _on(dev, stream) as raw:
+        if out is None:
+            out = torch.empty((rows, width), dtype=out_dtype or dout.dtype, device=dout.device)
+        ws_bytes = lib.muonh_embedding_grad_workspace(ids.numel(), rows, width)
+        ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dout.device)
+        rc = lib.muonh_embedding_grad(ids.data_ptr(), bits, ids.numel(), dout.data_ptr(), code, scale,
+                                      1 if accumulate else 0, out.data_ptr(), _code(out, "out"), rows, width,
+                                      ws.data_ptr(), ws_bytes, raw)
+    _check(rc, "muonh_embedding_grad")
+    return out
