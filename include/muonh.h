@@ -395,6 +395,43 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
                          size_t workspace_bytes, void* stream);
 
 /*
+ * muonh_cross_entropy -- softmax cross entropy of an output layer and both of
+ * its gradients, without the logits:
+ *   l_iv = <x_i, w_v>,  lse_i = log sum_v exp(l_iv)
+ *   token_loss_i = lse_i - l_i,t_i,    loss = c * sum_i token_loss_i
+ *   dx_i = s c sum_v P_iv w_v,  dw_v = s c sum_i P_iv x_i,
+ *   P_iv = exp(l_iv - lse_i) - [v = t_i]
+ * over the counted tokens: those whose target is in [0, rows) and not
+ * ignore_index.  c is 1 (MUONH_REDUCE_SUM) or 1 / the number of counted tokens
+ * (MUONH_REDUCE_MEAN), s is grad_scale.  Tokens that are not counted have token_loss
+ * and dx of zero and reach nothing else, whatever their x holds; with none
+ * counted the loss and both gradients are zero.
+ *   x           device, n x width, bf16;  w  device, rows x width, bf16
+ *   targets     device, n integers of id_bits (32 or 64), signed
+ *   n           0 .. 2^30; rows 1 .. 2^31 - 2; width 1 .. 65536 (MUONH_ENOTIMPL
+ *               above that, and above 2^31 tiles of 256 tokens x 256 rows)
+ *   loss        device, 1 float;  token_loss  device, n floats, or NULL
+ *   dx          device, n x width, bf16, or NULL (not computed)
+ *   dw          device, rows x width of dw_dtype (MUONH_BF16 / MUONH_F32), or
+ *               NULL; accumulate = 1 adds to it (gradient accumulation)
+ * Products take bf16 operands and sum in fp32.  The gradients see P rounded to
+ * bf16 (at most 2^-8 of each value off), also where dw is fp32.
+ * The vocabulary is taken in pieces for the gradients; the workspace decides
+ * how large: muonh_cross_entropy_workspace gives the size for a `limit` in
+ * bytes (0: pieces whose P takes up to 256 MiB; grads: 1 dx, 2 dw, 3 both; 0 is
+ * returned when the limit is below the smallest piece's need, or for invalid
+ * sizes; only the address of w matters, its alignment).  A row of w that is
+ * not a multiple of 64 values, or not on a 16-byte grid, is copied to the
+ * workspace once.
+ */
+enum { MUONH_REDUCE_MEAN = 0, MUONH_REDUCE_SUM = 1 };
+size_t muonh_cross_entropy_workspace(const void* w, int64_t n, int64_t rows, int64_t width, int grads, size_t limit);
+int muonh_cross_entropy(const void* x, const void* w, const void* targets, int id_bits, int64_t n, int64_t rows,
+                        int64_t width, int64_t ignore_index, int reduction, float grad_scale, float* loss,
+                        float* token_loss, void* dx, void* dw, int dw_dtype, int accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * Device flag counters, accumulated since the last reset:
  *   out[0] matrices whose orthogonalized update had zero norm,
  *   out[1] Hyperball radius restores (numerically zero post-update weight),

@@ -32,6 +32,8 @@ Around the step (``gradients.py``):
 * ``grad_norm(grads, max_norm=None)``, ``clip_grads(grads, max_norm, outputs=None)``
 * ``embedding(table, ids, scale=1.0, out=None, out_dtype=None)``,
   ``embedding_grad(ids, dout, rows, scale=1.0, out=None, out_dtype=None, accumulate=False)``
+* ``cross_entropy(x, w, targets, reduction="mean", grad=True, ...)``: the output
+  layer's loss with its gradients
 """
 from __future__ import annotations
 
@@ -47,6 +49,7 @@ MUONH_NS_FOLD, MUONH_NS_X32, MUONH_NS_H16 = 0, 1, 2
 _NS_PRECISION = {"fold": MUONH_NS_FOLD, "x32": MUONH_NS_X32, "h16": MUONH_NS_H16}
 MUONH_HOOK_HYPERBALL, MUONH_HOOK_RADIAL_BRAKE, MUONH_HOOK_NONE, MUONH_HOOK_RELATIVE = 0, 1, 2, 3
 MUONH_HB_STEP_UNIT, MUONH_HB_STEP_RADIUS = 0, 1
+MUONH_REDUCE_MEAN, MUONH_REDUCE_SUM = 0, 1
 
 EXPORTED = (
     "muonh_default_opts", "muonh_step", "muonh_step_noalloc", "adamh_step", "ns_orthogonalize", "frob_project", "muonh_get_flags",
@@ -54,6 +57,7 @@ EXPORTED = (
     "muonh_profile_begin", "muonh_profile_read", "muonh_version", "muonh_last_error",
     "muonh_grad_norm_workspace", "muonh_grad_norm", "muonh_clip_grads",
     "muonh_embedding", "muonh_embedding_grad_workspace", "muonh_embedding_grad",
+    "muonh_cross_entropy_workspace", "muonh_cross_entropy",
 )
 
 
@@ -178,6 +182,12 @@ def load(path: str = LIB_PATH):
     lib.muonh_embedding_grad.argtypes = [c_void_p, c_int, c_int64, c_void_p, c_int, c_float, c_int, c_void_p, c_int,
                                          c_int64, c_int64, c_void_p, c_size_t, c_void_p]
     lib.muonh_embedding_grad.restype = c_int
+    lib.muonh_cross_entropy_workspace.argtypes = [c_void_p, c_int64, c_int64, c_int64, c_int, c_size_t]
+    lib.muonh_cross_entropy_workspace.restype = c_size_t
+    lib.muonh_cross_entropy.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_int,
+                                        c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p,
+                                        c_size_t, c_void_p]
+    lib.muonh_cross_entropy.restype = c_int
     _LIB = lib
     return lib
 
@@ -466,4 +476,4 @@ def profile_read():
     return out
 
 
-from .gradients import clip_grads, embedding, embedding_grad, grad_norm  # noqa: E402,F401
+from .gradients import clip_grads, cross_entropy, embedding, embedding_grad, grad_norm  # noqa: E402,F401

@@ -12,6 +12,7 @@
 #include "grad.h"
 #include "muonh.h"
 #include "runtime.h"
+#include "xent.h"
 
 namespace muonh {
 namespace {
@@ -127,6 +128,80 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
   return p;
 }
 
+// ------------------------------------------------------------ cross entropy
+// Scratch of one call: what every call needs, then what the gradients need.
+struct XentPlan {
+  bool copy_w;
+  int64_t npad, rpad, wpad, wfull, cols, splits, pieces;
+  int64_t sc, xp, perm, tgt, lse, tlogit, wcopy, area, dxacc, bytes;
+};
+
+// P of one piece, in bytes, unless the caller sets a workspace limit.
+constexpr int64_t kXentPieceBytes = (int64_t)256 << 20;
+
+int check_xent(const void* w, int64_t n, int64_t rows, int64_t width) {
+  if (n < 0 || n > ((int64_t)1 << 30) || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;
+  if (width > kXMaxWidth) return MUONH_ENOTIMPL;
+  if (w && misaligned(w, 2)) return MUONH_EINVAL;
+  // tiles of one launch
+  if (up(n, kXTile) / kXTile * (up(rows, kXTile) / kXTile) > INT32_MAX) return MUONH_ENOTIMPL;
+  return MUONH_OK;
+}
+
+// Layout for a piece of `cols` words (0: no gradient).
+XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, int64_t cols) {
+  XentPlan p{};
+  // w's rows are an operand as they stand when they are whole stages on a
+  // 16-byte grid; else the call works on a padded copy
+  p.copy_w = width % kXStage != 0 || misaligned(w, 16);
+  p.npad = up(std::max<int64_t>(n, 1), kXTile);
+  p.rpad = up(rows, kXTile);
+  p.wpad = up(width, kXStage);
+  p.wfull = p.copy_w ? p.rpad : rows / kXTile * kXTile;
+  p.cols = cols;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  p.sc = take(sizeof(XentScalars));
+  p.xp = take(2 * p.npad * p.wpad);
+  p.perm = take(4 * p.npad);
+  p.tgt = take(4 * p.npad);
+  p.lse = take(4 * p.npad);
+  p.tlogit = take(4 * p.npad);
+  p.wcopy = take(2 * (p.copy_w ? p.rpad : p.rpad - p.wfull) * p.wpad);
+  // the statistics are read before the first piece's P is written
+  p.area = take(std::max<int64_t>(8 * (p.rpad / kXTile) * p.npad, 2 * p.npad * cols));
+  if (cols > 0) {
+    p.pieces = (p.rpad + cols - 1) / cols;
+    // dx jobs about as deep as dw's (the tokens), so that a launch's jobs are alike
+    p.splits = dx ? std::min<int64_t>(std::max<int64_t>(1, (cols + p.npad / 2) / p.npad), 8) : 1;
+    if (dx) p.dxacc = take(4 * p.splits * p.npad * p.wpad);
+  }
+  p.bytes = at;
+  return p;
+}
+
+// The largest piece whose layout fits `limit`; pieces are balanced.
+int xent_plan(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t limit, XentPlan& p) {
+  const int64_t npad = up(std::max<int64_t>(n, 1), kXTile), rpad = up(rows, kXTile);
+  if (!dx && !dw) {
+    p = xent_layout(w, n, rows, width, false, 0);
+    return p.bytes <= limit ? MUONH_OK : MUONH_ENOMEM;
+  }
+  int64_t tiles = std::max<int64_t>(1, std::min(rpad, kXentPieceBytes / (2 * npad)) / kXTile);
+  for (;;) {
+    const int64_t pieces = (rpad / kXTile + tiles - 1) / tiles;
+    tiles = (rpad / kXTile + pieces - 1) / pieces;
+    p = xent_layout(w, n, rows, width, dx, tiles * kXTile);
+    if (p.bytes <= limit) return MUONH_OK;
+    if (tiles == 1) return MUONH_ENOMEM;
+    tiles = std::max<int64_t>(1, tiles / 2);
+  }
+}
+
 }  // namespace
 }  // namespace muonh
 
@@ -240,6 +315,91 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
   const EmbedGradArgs a{u32(p.key[cur]), u32(p.pos[cur]), dout, dtable, reinterpret_cast<float*>(ws + p.part),
                         n, rows, width, scale, accumulate};
   MUONH_TRY_HIP(launch_embedding_grad(internal_dtype(dout_dtype), internal_dtype(dtable_dtype), a, s));
+  return MUONH_OK;
+}
+
+size_t muonh_cross_entropy_workspace(const void* w, int64_t n, int64_t rows, int64_t width, int grads, size_t limit) {
+  if (check_xent(w, n, rows, width) != MUONH_OK || grads < 0 || grads > 3) return 0;
+  XentPlan p;
+  const int64_t lim = limit ? (int64_t)std::min<size_t>(limit, (size_t)INT64_MAX) : INT64_MAX;
+  return xent_plan(w, n, rows, width, grads & 1, grads & 2, lim, p) == MUONH_OK ? (size_t)p.bytes : 0;
+}
+
+int muonh_cross_entropy(const void* x, const void* w, const void* targets, int id_bits, int64_t n, int64_t rows,
+                        int64_t width, int64_t ignore_index, int reduction, float grad_scale, float* loss,
+                        float* token_loss, void* dx, void* dw, int dw_dtype, int accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  int rc = check_xent(w, n, rows, width);
+  if (rc != MUONH_OK) return rc;
+  if (id_bits != 32 && id_bits != 64) return MUONH_EINVAL;
+  if (reduction != MUONH_REDUCE_MEAN && reduction != MUONH_REDUCE_SUM) return MUONH_EINVAL;
+  if (!std::isfinite(grad_scale) || bad_dtype(dw_dtype) || (accumulate != 0 && accumulate != 1)) return MUONH_EINVAL;
+  if (!w || !loss || misaligned(loss, 4) || misaligned(token_loss, 4)) return MUONH_EINVAL;
+  if (n > 0 && (!x || !targets || misaligned(x, 2) || misaligned(targets, id_bits / 8))) return MUONH_EINVAL;
+  if (misaligned(dx, 2) || misaligned(dw, dtype_size(dw_dtype))) return MUONH_EINVAL;
+  if (!workspace || misaligned(workspace, 256)) return MUONH_EINVAL;
+  XentPlan p;
+  rc = xent_plan(w, n, rows, width, dx != nullptr, dw != nullptr,
+                 (int64_t)std::min<size_t>(workspace_bytes, (size_t)INT64_MAX), p);
+  if (rc != MUONH_OK) return rc;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* const ws = reinterpret_cast<char*>(workspace);
+  auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+  auto f32 = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
+  XentArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = p.copy_w ? u16(p.wcopy) : static_cast<const uint16_t*>(w);
+  a.wtail = u16(p.wcopy);
+  a.targets = targets;
+  a.xp = u16(p.xp);
+  a.perm = reinterpret_cast<int32_t*>(ws + p.perm);
+  a.tgt = reinterpret_cast<int32_t*>(ws + p.tgt);
+  a.lse = f32(p.lse);
+  a.tlogit = f32(p.tlogit);
+  a.stats = reinterpret_cast<float2*>(ws + p.area);
+  a.prob = u16(p.area);
+  a.dxacc = f32(p.dxacc);
+  a.sc = reinterpret_cast<XentScalars*>(ws + p.sc);
+  a.loss = loss;
+  a.token_loss = token_loss;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw = dw;
+  a.n = n;
+  a.npad = p.npad;
+  a.rows = rows;
+  a.rpad = p.rpad;
+  a.wfull = p.wfull;
+  a.width = width;
+  a.wpad = p.wpad;
+  a.ldw = p.copy_w ? p.wpad : width;
+  a.ignore_index = ignore_index;
+  a.grad_scale = grad_scale;
+  a.id_bits = id_bits;
+  a.mean = reduction == MUONH_REDUCE_MEAN ? 1 : 0;
+  a.dw_dt = internal_dtype(dw_dtype);
+  a.accumulate = accumulate;
+  const double mac = 2.0 * (double)n * (double)rows * (double)width;
+  {
+    ProfScope pf(s, PC_XPREP, 0, 4.0 * (double)p.npad * (double)p.wpad);
+    MUONH_TRY_HIP(launch_xent_prepare(a, p.copy_w, static_cast<const uint16_t*>(w), s));
+  }
+  {
+    ProfScope pf(s, PC_XLOGIT, mac, 0);
+    MUONH_TRY_HIP(launch_xent_stats(a, s));
+  }
+  MUONH_TRY_HIP(launch_xent_loss(a, s));
+  if (!dx && !dw) return MUONH_OK;
+  for (int64_t v0 = 0; v0 < p.rpad; v0 += p.cols) {
+    const XentPiece pc{v0, std::min(p.cols, p.rpad - v0), (int32_t)p.splits, v0 == 0 ? 1 : 0};
+    const double share = (double)pc.cols / (double)p.rpad;
+    {
+      ProfScope pf(s, PC_XPROB, mac * share, 0);
+      MUONH_TRY_HIP(launch_xent_prob(a, pc, s));
+    }
+    ProfScope pf(s, PC_XGRAD, ((dx ? 1 : 0) + (dw ? 1 : 0)) * mac * share, 0);
+    MUONH_TRY_HIP(launch_xent_grad(a, pc, s));
+  }
+  if (dx && n > 0) MUONH_TRY_HIP(launch_xent_dx(a, (int)p.splits, s));
   return MUONH_OK;
 }
 

@@ -1,0 +1,699 @@
+// Softmax cross entropy of an output layer with its gradient (gfx950).
+//
+//   l_iv   = <x_i, w_v>,   lse_i = log sum_v exp(l_iv),   loss_i = lse_i - l_i,t_i
+//   P_iv   = exp(l_iv - lse_i) - [v = t_i]
+//   dx_i   = c sum_v P_iv w_v,     dw_v = c sum_i P_iv x_i
+//
+// over the counted tokens only (target inside [0, rows) and not ignore_index):
+// they are gathered to the front of a padded copy of x, so that ignored tokens
+// cost no product and whatever they hold reaches nothing.
+//
+// The logits are never stored.  A first product over the whole vocabulary
+// keeps, per token and tile of 256 words, the maximum and the sum of exponents
+// (k_xent_logits, STATS); they give lse and the loss.  The gradient then takes
+// the vocabulary in pieces: the same product again, its epilogue turning the
+// logits into P in bf16 (off by at most 2^-8 of each value; the operand type of the
+// matrix cores) for one piece, and two products that read that P:
+// dx += P w_piece (fp32 across pieces) and dw_piece = P^T x.
+//
+// All products run on one 256 x 256 main loop of 8 waves, D[m][n] =
+// sum_k A[m][k] B[n][k]: v_mfma_f32_32x32x16_bf16, 64-deep operand stages
+// double buffered in LDS, brought in by direct global -> LDS loads; the two
+// waves of a SIMD alternate between reading fragments and running MFMAs.  An
+// operand whose rows run along k is read as it is; one stored [k][m] is read
+// through gfx950's transposing LDS read, so neither P, x nor w is ever
+// transposed in memory.  The side a lane holds four consecutive values of (m)
+// is the one the result's rows run along: words for P, width for dx and dw.
+#include "common.h"
+#include "xent.h"
+
+namespace muonh {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef short i16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+
+constexpr int kXThreads = 512;
+constexpr int kOperand = kXTile * kXStage;        // elements of one operand stage
+constexpr int kOperandB = kOperand * 2;           // 32 KiB
+constexpr int kXSmem = 4 * kOperandB;             // two stages of two operands
+constexpr int WM = 64, WN = 128;                  // a wave's block: 4 x 2 waves
+constexpr int MI = WM / 32, NI = WN / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0)
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }     // lgkmcnt(0)
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Chunk c (16 bytes) of a k-contiguous LDS row r sits at c ^ swz(r): any 16
+// consecutive rows of one chunk are spread over all banks.
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// One operand of the product: TR false, 256 rows of k-contiguous values (row
+// stride ld elements); TR true, k rows of 256 values along m.
+template <bool TR>
+struct Operand {
+  uint32_t voff;      // this lane's byte offset of the wave's first 1 KiB run
+  uint32_t rstride;   // bytes between its runs
+  // ncols (TR): columns of the operand from the tile's first one; chunks past
+  // them are read from the last one and only reach results that are not kept
+  __device__ __forceinline__ void init(int wv4, int lane, int64_t ld, int64_t ncols) {
+    if constexpr (TR) {
+      const int k = 2 * wv4 + (lane >> 5), pc = lane & 31;
+      const int c = (pc - 4 * (k & 3)) & 31;  // row k is rotated by 4 (k % 4) chunks
+      const int64_t col = min((int64_t)c * 8, ncols - 8);
+      voff = (uint32_t)((k * ld + col) * 2);
+      rstride = (uint32_t)(8 * ld * 2);
+    } else {
+      const int r = 8 * wv4 + lane / 8, pc = lane % 8;
+      voff = (uint32_t)((r * ld + (pc ^ swz(r)) * 8) * 2);
+      rstride = (uint32_t)(32 * ld * 2);
+    }
+  }
+};
+
+template <bool TR>
+__device__ __forceinline__ int frag_base(int wave_row, int lane) {
+  if constexpr (TR) {
+    const int j = lane & 15, g = lane >> 4;
+    const int k = 8 * (g >> 1) + (j >> 2);
+    return k * kXTile + ((wave_row + 16 * (g & 1) + 4 * (j & 3) + 32 * (j >> 2)) & (kXTile - 1));
+  } else {
+    return (wave_row + (lane & 31)) * kXStage;
+  }
+}
+
+// Fragment of k-step kk (16 deep): 8 consecutive k of one row per lane.
+template <bool TR>
+__device__ __forceinline__ bf16x8_t frag(const uint16_t* stage, int base, int xk, int kk) {
+  if constexpr (TR) {
+    const uint16_t* p = stage + base + kk * 16 * kXTile;
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)p);
+    const i16x4_t hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p + 4 * kXTile));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    return *reinterpret_cast<const bf16x8_t*>(stage + base + xk);
+  }
+}
+
+// acc = sum over nstage stages.  abase(s) / bbase(s): address of the tile's
+// first value of stage s (uniform).  Waves 0-3 load operand A, waves 4-7
+// operand B; the groups run one phase apart, each phase (a half stage's
+// fragments, or its MFMAs) ending at a barrier of all 8 waves, so that of the
+// two waves on a SIMD one always feeds the matrix core.  Stage s + 1
+// overwrites the buffer of stage s - 1, whose last fragments were read in
+// phase 4 s - 1; its loads ride between the MFMAs of phases 4 s and 4 s + 1
+// and are waited for at the end of phase 4 s + 3, before their first use.
+template <bool TRA, bool TRB, typename FA, typename FB>
+__device__ __forceinline__ void product(char* smem, int nstage, FA&& abase, int64_t lda, int64_t acols, FB&& bbase,
+                                        int64_t ldb, int64_t bcols, f32x16_t (&acc)[MI][NI]) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wv >> 2, wm = wv >> 1, wn = wv & 1;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  if (nstage <= 0) return;
+  uint32_t voff, rstride;
+  if (grp == 0) {
+    Operand<TRA> o;
+    o.init(wv & 3, lane, lda, acols);
+    voff = o.voff;
+    rstride = o.rstride;
+  } else {
+    Operand<TRB> o;
+    o.init(wv & 3, lane, ldb, bcols);
+    voff = o.voff;
+    rstride = o.rstride;
+  }
+  const int half = grp * kOperandB + (wv & 3) * 1024;
+  auto stage_base = [&](int s) -> const char* {
+    return reinterpret_cast<const char*>(grp == 0 ? abase(s) : bbase(s));
+  };
+  // run (wave % 4) + 4 p of a stage of this wave's operand
+  auto load_run = [&](const char* src, int s, int p) {
+    __builtin_amdgcn_global_load_lds(
+        (MUONH_GLOBAL void*)(gmem(src + (int64_t)p * rstride) + voff),
+        (__attribute__((address_space(3))) void*)(smem + (s & 1) * 2 * kOperandB + half + 4 * p * 1024), 16, 0, 0);
+  };
+  auto load_stage = [&](int s) {
+    const char* src = stage_base(s);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) load_run(src, s, p);
+  };
+  int xk[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) xk[kk] = ((2 * kk + (lane >> 5)) ^ swz(lane & 31)) * 8;
+  int ab[MI], bb[NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) ab[i] = frag_base<TRA>(wm * WM + i * 32, lane);
+#pragma unroll
+  for (int j = 0; j < NI; ++j) bb[j] = frag_base<TRB>(wn * WN + j * 32, lane);
+  bf16x8_t fa[2][MI], fb[2][NI];
+  auto read_half = [&](int s, int h) {
+    const uint16_t* sa = reinterpret_cast<const uint16_t*>(smem + (s & 1) * 2 * kOperandB);
+    const uint16_t* sb = sa + kOperand;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int kk = 2 * h + q;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[q][i] = frag<TRA>(sa, ab[i], xk[kk], kk);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[q][j] = frag<TRB>(sb, bb[j], xk[kk], kk);
+    }
+  };
+  // a half stage's 16 MFMAs, with this wave's loads of stage ls in between
+  auto mma_half = [&](int ls) {
+    const char* src = ls >= 0 ? stage_base(ls) : nullptr;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int t = 0; t < 2 * MI * NI; ++t) {
+      const int q = t / (MI * NI), i = (t / NI) % MI, j = t % NI;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[q][i], fb[q][j], acc[i][j], 0, 0, 0);
+      if (t & 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (ls >= 0) load_run(src, ls, t / 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load_stage(0);
+  wait_loads();
+  barrier();
+  if (grp == 0) {
+    for (int s = 0; s < nstage; ++s) {
+      read_half(s, 0);                           // phase 4 s
+      wait_lds();
+      barrier();
+      mma_half(s + 1 < nstage ? s + 1 : -1);     // phase 4 s + 1
+      barrier();
+      read_half(s, 1);                           // phase 4 s + 2
+      wait_lds();
+      barrier();
+      mma_half(-1);                              // phase 4 s + 3
+      wait_loads();
+      barrier();
+    }
+  } else {
+    for (int s = 0; s < nstage; ++s) {
+      if (s > 0) mma_half(s + 1 < nstage ? s + 1 : -1);  // phase 4 s
+      else if (nstage > 1) load_stage(1);
+      barrier();
+      read_half(s, 0);                           // phase 4 s + 1
+      wait_lds();
+      barrier();
+      mma_half(-1);                              // phase 4 s + 2
+      barrier();
+      read_half(s, 1);                           // phase 4 s + 3
+      wait_lds();
+      wait_loads();
+      barrier();
+    }
+    mma_half(-1);
+  }
+}
+
+// Job order: hardware deals workgroups round-robin over the 8 XCDs; each XCD
+// gets a contiguous run of the job list, whose neighbours share operand panels
+// in its L2.
+__device__ __forceinline__ int xcd_job(int bid, int njobs) {
+  const int q = njobs / 8, rem = njobs % 8, xcd = bid % 8, loc = bid / 8;
+  return xcd * q + min(xcd, rem) + loc;
+}
+
+// Job -> (row tile, column tile) with 8 row tiles at a time running over all
+// columns, so that 32 neighbouring jobs form an 8 x 4 block.
+__device__ __forceinline__ void block_order(int job, int nr, int nc, int& r, int& c) {
+  const int per = 8 * nc, band = job / per;
+  const int h = min(8, nr - band * 8), in = job - band * per;
+  c = in / h;
+  r = band * 8 + in - c * h;
+}
+
+// Address of row v of the weights; rows from full on are in the padded copy.
+__device__ __forceinline__ const uint16_t* w_row(const uint16_t* w, const uint16_t* tail, int64_t full, int64_t ld,
+                                                 int64_t v) {
+  return v < full ? w + v * ld : tail + (v - full) * ld;
+}
+
+// ---------------------------------------------------------------------------
+// logits of a 256-word x 256-token tile: statistics (first pass) or P
+// ---------------------------------------------------------------------------
+template <bool STATS>
+__global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_logits(
+    const XentArgs a, const XentPiece p, int ntok, int nvoc) {
+  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
+  int tt, tv;
+  block_order(xcd_job(blockIdx.x, ntok * nvoc), ntok, nvoc, tt, tv);
+  const int count = a.sc->count;
+  const int64_t tok0 = (int64_t)tt * kXTile;
+  if (tok0 >= count) return;
+  const int64_t v0 = p.v0 + (int64_t)tv * kXTile;
+  f32x16_t acc[MI][NI];
+  const uint16_t* const wt = w_row(a.w, a.wtail, a.wfull, a.ldw, v0);
+  const uint16_t* const xt = a.xp + tok0 * a.wpad;
+  product<false, false>(
+      smem, (int)(a.wpad / kXStage), [=](int s) { return wt + s * kXStage; }, a.ldw, 0,
+      [=](int s) { return xt + s * kXStage; }, a.wpad, 0, acc);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int hi = lane >> 5;
+  const int64_t vw = v0 + wm * WM;                   // the wave's first word
+  const int words = (int)min<int64_t>(WM, a.rows - vw);  // of them real (may be <= 0)
+  // word of acc[i][.][v], counted from vw
+  auto word = [&](int i, int v) { return i * 32 + 8 * (v >> 2) + 4 * hi + (v & 3); };
+  if constexpr (STATS) {
+    float2* const st = reinterpret_cast<float2*>(smem);  // [4][256]
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int tl = wn * WN + j * 32 + (lane & 31);
+      if (words < WM) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (word(i, v) >= words) acc[i][j][v] = -INFINITY;
+      }
+      float m = acc[0][j][0];
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      const float mb = m == -INFINITY ? 0.f : m * kLog2e;  // nothing finite: the sum is 0
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -mb));
+      s += __shfl_xor(s, 32, 64);
+      if (hi == 0) st[wm * kXTile + tl] = make_float2(m, s);
+      // the target's logit, where this wave holds it
+      const int64_t ci = tok0 + tl;
+      const int64_t t = ci < count ? (int64_t)a.tgt[ci] - vw : -1;
+      const bool have = t >= 0 && t < WM && ((t >> 2) & 1) == hi;
+      if (__ballot(have)) {
+        float l = 0.f;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) l = word(i, v) == t ? acc[i][j][v] : l;
+        if (have) a.tlogit[ci] = l;
+      }
+    }
+    __syncthreads();
+    if (tid < kXTile) {
+      float m = st[tid].x;
+#pragma unroll
+      for (int k = 1; k < 4; ++k) m = fmaxf(m, st[k * kXTile + tid].x);
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 q = st[k * kXTile + tid];
+        s += q.x == -INFINITY ? q.y : q.y * __builtin_amdgcn_exp2f((q.x - m) * kLog2e);
+      }
+      a.stats[(v0 / kXTile) * a.npad + tok0 + tid] = make_float2(m, s);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
+      const bool in = ci < count;
+      const float lb = in ? a.lse[ci] * kLog2e : 0.f;
+      const int64_t t = in ? (int64_t)a.tgt[ci] - vw : -1;
+      uint16_t* const row = a.prob + ci * p.cols + (vw - p.v0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int pq = 0; pq < 2; ++pq) {
+          float e[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int v = 4 * (2 * pq + h) + k, wd = word(i, v);
+              float q = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
+              q = wd == t ? q - 1.f : q;
+              e[h][k] = in && wd < words ? q : 0.f;
+            }
+          // lanes l and l + 32 trade groups: each then holds 8 consecutive words
+          const uint32_t w0 = pack_bf16x2(e[0][0], e[0][1]), w1 = pack_bf16x2(e[0][2], e[0][3]);
+          const uint32_t w2 = pack_bf16x2(e[1][0], e[1][1]), w3 = pack_bf16x2(e[1][2], e[1][3]);
+          const auto s0 = __builtin_amdgcn_permlane32_swap(w0, w2, false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(w1, w3, false, false);
+          const u32x4_t pk = {s0[0], s1[0], s0[1], s1[1]};
+          *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(row + i * 32 + 16 * pq + 8 * hi)) = pk;
+        }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradients of one piece: jobs [0, ndw) are dw tiles (256 of width x 256
+// words, depth = tokens), the rest dx tiles (256 of width x 256 tokens, depth
+// = one split of the piece's words)
+// ---------------------------------------------------------------------------
+template <typename WT>
+__global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_grad(
+    const XentArgs a, const XentPiece p, int ndw, int ndx, int nd) {
+  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
+  const int count = a.sc->count;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int hi = lane >> 5;
+  f32x16_t acc[MI][NI];
+  if ((int)blockIdx.x < ndw) {
+    int tv, td;
+    block_order(xcd_job(blockIdx.x, ndw), ndw / nd, nd, tv, td);
+    const int64_t d0 = (int64_t)td * kXTile, vl = (int64_t)tv * kXTile;  // word in the piece
+    const uint16_t* const xt = a.xp + d0;
+    const uint16_t* const pt = a.prob + vl;
+    const int64_t ldx = a.wpad, ldp = p.cols;
+    product<true, true>(
+        smem, (count + kXStage - 1) / kXStage, [=](int s) { return xt + (int64_t)s * kXStage * ldx; }, ldx, ldx - d0,
+        [=](int s) { return pt + (int64_t)s * kXStage * ldp; }, ldp, ldp - vl, acc);
+    const float g = a.sc->gscale;
+    WT* const dw = reinterpret_cast<WT*>(a.dw);
+    const bool vec = a.width % 8 == 0 && (uintptr_t)dw % 16 == 0;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int64_t v = p.v0 + vl + wn * WN + j * 32 + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int pq = 0; pq < 2; ++pq) {
+          float e[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * pq + k] * g),
+                                                             __float_as_uint(acc[i][j][8 * pq + 4 + k] * g), false, false);
+            e[k] = __uint_as_float(sw[0]);
+            e[4 + k] = __uint_as_float(sw[1]);
+          }
+          const int64_t d = d0 + wm * WM + i * 32 + 16 * pq + 8 * hi;
+          if (v >= a.rows || d >= a.width) continue;
+          const int64_t at = v * a.width + d;
+          if (vec) {
+            if (a.accumulate) {
+              float old[8];
+              load8(dw, at, old);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) e[k] += old[k];
+            }
+            store8(dw, at, e);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (d + k < a.width) St<WT>::st(dw, at + k, a.accumulate ? e[k] + St<WT>::ld(dw, at + k) : e[k]);
+          }
+        }
+    }
+    return;
+  }
+  const int job = xcd_job(blockIdx.x - ndw, ndx);
+  const int per = ndx / p.splits, split = job / per;
+  int tt, td;
+  block_order(job - split * per, per / nd, nd, tt, td);
+  const int64_t tok0 = (int64_t)tt * kXTile, d0 = (int64_t)td * kXTile;
+  if (tok0 >= count) return;
+  // this split's stages of the piece
+  const int64_t all = p.cols / kXStage;
+  const int s0 = (int)(all * split / p.splits), s1 = (int)(all * (split + 1) / p.splits);
+  const uint16_t* const pt = a.prob + tok0 * p.cols + (int64_t)s0 * kXStage;
+  const uint16_t *const w = a.w + d0, *const tail = a.wtail + d0;
+  const int64_t ldw = a.ldw, full = a.wfull, vs = p.v0 + (int64_t)s0 * kXStage;
+  product<true, false>(
+      smem, s1 - s0, [=](int s) { return w_row(w, tail, full, ldw, vs + (int64_t)s * kXStage); }, ldw, a.wpad - d0,
+      [=](int s) { return pt + (int64_t)s * kXStage; }, p.cols, 0, acc);
+  float* const out = a.dxacc + (int64_t)split * a.npad * a.wpad;
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t d = d0 + wm * WM + i * 32 + 8 * q + 4 * hi;
+        if (d >= a.wpad) continue;
+        f32x4_t e = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        MUONH_GLOBAL f32x4_t* const o = reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(out + ci * a.wpad + d));
+        if (!p.first) e += *o;
+        *o = e;
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// around the products
+// ---------------------------------------------------------------------------
+// One workgroup: the list of counted tokens in batch order, and the factors.
+constexpr int kIndexThreads = 1024;
+__global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) {
+  __shared__ int32_t wsum[kIndexThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int PER = 8;
+  int64_t base = 0;
+  for (int64_t i0 = 0; i0 < a.n; i0 += kIndexThreads * PER) {
+    int32_t t[PER];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t i = i0 + tid * PER + k;
+      int64_t v = -1;
+      if (i < a.n)
+        v = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[i]
+                            : gmem(reinterpret_cast<const int64_t*>(a.targets))[i];
+      const bool in = i < a.n && v >= 0 && v < a.rows && v != a.ignore_index;
+      t[k] = in ? (int32_t)v : -1;
+      mine += in;
+      if (i < a.n && !in && a.token_loss != nullptr) a.token_loss[i] = 0.f;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 63) wsum[wave] = incl;
+    __syncthreads();
+    int64_t at = base + incl - mine;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kIndexThreads / 64; ++w) {
+      if (w < wave) at += wsum[w];
+      total += wsum[w];
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (t[k] >= 0) {
+        a.perm[at] = (int32_t)(i0 + tid * PER + k);
+        a.tgt[at] = t[k];
+        ++at;
+      }
+    base += total;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    const double c = a.mean ? 1.0 / (double)max<int64_t>(base, 1) : 1.0;
+    a.sc->count = (int32_t)base;
+    a.sc->scale = (float)c;
+    a.sc->gscale = (float)(c * (double)a.grad_scale);
+  }
+}
+
+// Rows of `width` values copied to rows of `ld`, zero padded: element e of an
+// 8-element chunk past the row or its end is 0.
+__device__ __forceinline__ void copy_chunk(const uint16_t* src, bool row_ok, int64_t width, bool vec, int64_t col,
+                                           uint16_t* dst) {
+  u32x4_t q = {0u, 0u, 0u, 0u};
+  if (row_ok) {
+    if (vec && col + 8 <= width) {
+      q = *reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(src + col));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t v = col + e < width ? (uint32_t)gmem(src)[col + e] : 0u;
+        q[e / 2] |= v << (16 * (e & 1));
+      }
+    }
+  }
+  *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(dst + col)) = q;
+}
+
+// Blocks [0, npad): one row of xp each (counted tokens of x, then zeros); the
+// others: one row of the padded copy of the weights from row w0 on.
+__global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uint16_t* w_in, uint16_t* w_out,
+                                                     int64_t w0) {
+  const int64_t b = blockIdx.x;
+  if (b < a.npad) {
+    const bool ok = b < a.sc->count;
+    const uint16_t* const src = a.x + (ok ? (int64_t)a.perm[b] : 0) * a.width;
+    const bool vec = a.width % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+    for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8) copy_chunk(src, ok, a.width, vec, c, a.xp + b * a.wpad);
+    return;
+  }
+  const int64_t r = b - a.npad, v = w0 + r;
+  const bool vec = a.width % 8 == 0 && (uintptr_t)w_in % 16 == 0;
+  for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8)
+    copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, vec, c, w_out + r * a.wpad);
+}
+
+// lse and loss of each counted token from its tiles' statistics.
+__global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
+  // 32 tokens a block; 8 threads share a token's tiles
+  __shared__ float2 sh[8][32];
+  const int tl = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int64_t ci = (int64_t)blockIdx.x * 32 + tl;
+  const int count = a.sc->count;
+  if ((int64_t)blockIdx.x * 32 >= count) return;
+  const int64_t tiles = a.rpad / kXTile;
+  float m = -INFINITY, s = 0.f;
+  for (int64_t k = part; k < tiles; k += 8) {
+    const float2 q = a.stats[k * a.npad + ci];
+    const float nm = fmaxf(m, q.x);
+    if (nm != -INFINITY) {
+      s = s * __builtin_amdgcn_exp2f((m - nm) * kLog2e) + q.y * __builtin_amdgcn_exp2f((q.x - nm) * kLog2e);
+      m = nm;
+    } else {
+      s += q.y;  // 0, or a NaN to pass on
+    }
+  }
+  sh[part][tl] = make_float2(m, s);
+  __syncthreads();
+  if (part == 0 && ci < count) {
+    float mm = sh[0][tl].x;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) mm = fmaxf(mm, sh[k][tl].x);
+    double t = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 q = sh[k][tl];
+      t += q.x == -INFINITY ? (double)q.y : (double)q.y * (double)__builtin_amdgcn_exp2f((q.x - mm) * kLog2e);
+    }
+    const float l = mm + logf((float)t);
+    a.lse[ci] = l;
+    const float loss = l - a.tlogit[ci];
+    a.tlogit[ci] = loss;  // summed by k_xent_total
+    if (a.token_loss != nullptr) a.token_loss[a.perm[ci]] = loss;
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_xent_total(const XentArgs a) {
+  __shared__ double red[16];
+  const int count = a.sc->count;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += 1024) s += (double)a.tlogit[i];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += red[k];
+    a.loss[0] = (float)(a.mean ? v / (double)max(count, 1) : v);
+  }
+}
+
+// dx: the splits' sums in order, scaled and rounded; ignored tokens get zeros.
+// Block b < npad handles row b of dxacc; the row of an ignored token is
+// written by the blocks after them, one a token.
+__global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
+  const int64_t b = blockIdx.x;
+  const bool vec = a.width % 8 == 0 && (uintptr_t)a.dx % 16 == 0;
+  const int count = a.sc->count;
+  int64_t token;
+  bool zero = false;
+  if (b < a.n) {  // rows of dxacc
+    if (b >= count) return;
+    token = a.perm[b];
+  } else {
+    token = b - a.n;
+    const int64_t v = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[token]
+                                      : gmem(reinterpret_cast<const int64_t*>(a.targets))[token];
+    if (v >= 0 && v < a.rows && v != a.ignore_index) return;
+    zero = true;
+  }
+  const float g = a.sc->gscale;
+  for (int64_t c = threadIdx.x * 8; c < a.width; c += 256 * 8) {
+    float e[8] = {};
+    if (!zero) {
+      for (int k = 0; k < splits; ++k) {
+        float q[8];
+        load8(a.dxacc, ((int64_t)k * a.npad + b) * a.wpad + c, q);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) e[x] += q[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) e[x] *= g;
+    }
+    const int64_t at = token * a.width + c;
+    if (vec) store8(a.dx, at, e);
+    else
+      for (int x = 0; x < 8; ++x)
+        if (c + x < a.width) St<bf16_t>::st(a.dx, at + x, e[x]);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w_in, hipStream_t s) {
+  hipLaunchKernelGGL(k_xent_index, dim3(1), dim3(kIndexThreads), 0, s, a);
+  // the whole of w where its rows are no operand as they stand, else its last tile
+  const int64_t w0 = copy_w ? 0 : a.wfull;
+  uint16_t* const w_out = const_cast<uint16_t*>(copy_w ? a.w : a.wtail);
+  const int64_t wrows = copy_w ? a.rpad : a.rpad - a.wfull;
+  hipLaunchKernelGGL(k_xent_gather, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_stats(const XentArgs& a, hipStream_t s) {
+  const int ntok = (int)(a.npad / kXTile), nvoc = (int)(a.rpad / kXTile);
+  const XentPiece p{0, a.rpad, 1, 1};
+  hipLaunchKernelGGL((k_xent_logits<true>), dim3(ntok * nvoc), dim3(kXThreads), 0, s, a, p, ntok, nvoc);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_loss(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(k_xent_lse, dim3(a.npad / 32), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_xent_total, dim3(1), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_prob(const XentArgs& a, const XentPiece& p, hipStream_t s) {
+  const int ntok = (int)(a.npad / kXTile), nvoc = (int)(p.cols / kXTile);
+  hipLaunchKernelGGL((k_xent_logits<false>), dim3(ntok * nvoc), dim3(kXThreads), 0, s, a, p, ntok, nvoc);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_grad(const XentArgs& a, const XentPiece& p, hipStream_t s) {
+  const int nd = (int)((a.wpad + kXTile - 1) / kXTile);
+  const int ndw = a.dw ? (int)(p.cols / kXTile) * nd : 0;
+  const int ndx = a.dx ? (int)(a.npad / kXTile) * nd * p.splits : 0;
+  if (a.dw_dt == DT_BF16)
+    hipLaunchKernelGGL((k_xent_grad<bf16_t>), dim3(ndw + ndx), dim3(kXThreads), 0, s, a, p, ndw, ndx, nd);
+  else
+    hipLaunchKernelGGL((k_xent_grad<float>), dim3(ndw + ndx), dim3(kXThreads), 0, s, a, p, ndw, ndx, nd);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_dx(const XentArgs& a, int splits, hipStream_t s) {
+  hipLaunchKernelGGL(k_xent_dx, dim3(2 * a.n), dim3(256), 0, s, a, splits);
+  return hipGetLastError();
+}
+
+}  // namespace muonh

@@ -1,5 +1,5 @@
 """The gradients an optimizer step consumes: their global norm and clipping, the
-embedding and its gradient.
+embedding and its gradient, the output layer's loss with its gradients.
 
 Argument marshalling only, like the rest of the binding: the work is queued on
 ``stream`` (default: the current stream of the tensors' device) and never waits
@@ -16,7 +16,8 @@ from ctypes import c_void_p
 
 import torch
 
-from . import MUONH_BF16, MUONH_F32, MuonhError, load
+from . import (MUONH_BF16, MUONH_ENOMEM, MUONH_F32, MUONH_REDUCE_MEAN, MUONH_REDUCE_SUM, MuonhError,
+               load)
 
 _CODE = {torch.float32: MUONH_F32, torch.bfloat16: MUONH_BF16}
 
@@ -216,3 +217,75 @@ def embedding_grad(ids, dout, rows=None, scale=1.0, out=None, out_dtype=None, ac
                                       ws.data_ptr(), ws_bytes, raw)
     _check(rc, "muonh_embedding_grad")
     return out
+
+
+_REDUCTION = {"mean": MUONH_REDUCE_MEAN, "sum": MUONH_REDUCE_SUM}
+
+
+def cross_entropy(x, w, targets, reduction="mean", grad=True, grad_scale=1.0, ignore_index=-100, dx=None, dw=None,
+                  dw_dtype=None, accumulate=False, workspace_limit=0, stream=None):
+    """Softmax cross entropy of ``x @ w.T`` with its gradients, without the logits.
+
+    ``x``: ``targets.shape + (width,)``, bfloat16; ``w``: rows x width, bfloat16;
+    ``targets``: int64 / int32.  Tokens whose target is ``ignore_index`` or
+    outside ``[0, rows)`` are not counted: they have no loss and no gradient.
+    ``reduction``: "mean" over the counted tokens, or "sum".
+
+    Returns ``(loss, token_loss, dx, dw)``: the loss and the loss of every token
+    in float32, and the gradients times ``grad_scale`` (``None`` with
+    ``grad=False``).  ``grad`` may also be "x" or "w" for one of the two.
+    ``dx`` (bfloat16) and ``dw`` (bfloat16 or float32, ``dw_dtype``) are
+    allocated unless given; ``accumulate`` adds to the given ``dw``.
+    ``workspace_limit`` (bytes) bounds the scratch memory: the vocabulary is
+    taken in pieces that fit it.
+    """
+    if reduction not in _REDUCTION:
+        raise ValueError(f"reduction must be 'mean' or 'sum', got {reduction!r}")
+    if grad not in (True, False, "x", "w"):
+        raise ValueError("grad must be True, False, 'x' or 'w'")
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix (2-D)")
+    dev = _plain(x, "x")
+    _plain(w, "w", dev)
+    _plain(targets, "targets", dev)
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("x and w must be torch.bfloat16")
+    bits = _id_bits(targets, "targets")
+    rows, width = w.shape
+    if tuple(x.shape) != (*targets.shape, width):
+        raise ValueError("x must have the shape of targets and w's width")
+    want_x, want_w = grad in (True, "x"), grad in (True, "w")
+    if (dx is not None and not want_x) or (dw is not None and not want_w):
+        raise ValueError("an output is given for a gradient that is not asked for")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    if dx is not None:
+        _plain(dx, "dx", dev)
+        if dx.shape != x.shape or dx.dtype != torch.bfloat16:
+            raise ValueError("dx must match x in shape and dtype")
+    if dw is not None:
+        _plain(dw, "dw", dev)
+        if dw.shape != w.shape or (dw_dtype is not None and dw.dtype != dw_dtype):
+            raise ValueError("dw must match w in shape, and dw_dtype")
+    n = targets.numel()
+    lib = load()
+    with _on(dev, stream) as raw:
+        if want_x and dx is None:
+            dx = torch.empty_like(x)
+        if want_w and dw is None:
+            dw = torch.empty_like(w, dtype=dw_dtype or torch.bfloat16)
+        code = MUONH_BF16 if dw is None else _code(dw, "dw")
+        grads = (1 if want_x else 0) + (2 if want_w else 0)
+        ws_bytes = lib.muonh_cross_entropy_workspace(w.data_ptr(), n, rows, width, grads, workspace_limit)
+        if ws_bytes == 0 and workspace_limit and lib.muonh_cross_entropy_workspace(w.data_ptr(), n, rows, width, grads, 0):
+            raise MuonhError(MUONH_ENOMEM, "muonh_cross_entropy")
+        ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=x.device)
+        loss = torch.empty((), dtype=torch.float32, device=x.device)
+        token_loss = torch.empty(targets.shape, dtype=torch.float32, device=x.device)
+        rc = lib.muonh_cross_entropy(x.data_ptr(), w.data_ptr(), targets.data_ptr(), bits, n, rows, width, ignore_index,
+                                     _REDUCTION[reduction], grad_scale, loss.data_ptr(),
+                                     token_loss.data_ptr() if n else None, dx.data_ptr() if want_x else None,
+                                     dw.data_ptr() if want_w else None, code, 1 if accumulate else 0, ws.data_ptr(),
+                                     ws_bytes, raw)
+    _check(rc, "muonh_cross_entropy")
+    return loss, token_loss, dx, dw
