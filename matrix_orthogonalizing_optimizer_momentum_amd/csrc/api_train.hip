@@ -132,8 +132,8 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
 // Scratch of one call: what every call needs, then what the gradients need.
 struct XentPlan {
   bool copy_w;
-  int64_t npad, rpad, wpad, wfull, cols, splits, pieces;
-  int64_t sc, xp, perm, tgt, lse, tlogit, wcopy, area, dxacc, bytes;
+  int64_t npad, rpad, wpad, wfull, ldxt, cols, splits, pieces;
+  int64_t sc, xp, xt, perm, tgt, lse, tlogit, wcopy, area, dxacc, bytes;
 };
 
 // P of one piece, in bytes, unless the caller sets a workspace limit.
@@ -149,7 +149,7 @@ int check_xent(const void* w, int64_t n, int64_t rows, int64_t width) {
 }
 
 // Layout for a piece of `cols` words (0: no gradient).
-XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, int64_t cols) {
+XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t cols) {
   XentPlan p{};
   // w's rows are an operand as they stand when they are whole stages on a
   // 16-byte grid; else the call works on a padded copy
@@ -167,6 +167,8 @@ XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool
   };
   p.sc = take(sizeof(XentScalars));
   p.xp = take(2 * p.npad * p.wpad);
+  p.ldxt = p.npad + 128;  // off the powers of two, so that rows fall on different memory channels
+  p.xt = take(dw ? 2 * up(p.wpad, kXTile) * p.ldxt : 0);
   p.perm = take(4 * p.npad);
   p.tgt = take(4 * p.npad);
   p.lse = take(4 * p.npad);
@@ -188,14 +190,14 @@ XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool
 int xent_plan(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t limit, XentPlan& p) {
   const int64_t npad = up(std::max<int64_t>(n, 1), kXTile), rpad = up(rows, kXTile);
   if (!dx && !dw) {
-    p = xent_layout(w, n, rows, width, false, 0);
+    p = xent_layout(w, n, rows, width, false, false, 0);
     return p.bytes <= limit ? MUONH_OK : MUONH_ENOMEM;
   }
   int64_t tiles = std::max<int64_t>(1, std::min(rpad, kXentPieceBytes / (2 * npad)) / kXTile);
   for (;;) {
     const int64_t pieces = (rpad / kXTile + tiles - 1) / tiles;
     tiles = (rpad / kXTile + pieces - 1) / pieces;
-    p = xent_layout(w, n, rows, width, dx, tiles * kXTile);
+    p = xent_layout(w, n, rows, width, dx, dw, tiles * kXTile);
     if (p.bytes <= limit) return MUONH_OK;
     if (tiles == 1) return MUONH_ENOMEM;
     tiles = std::max<int64_t>(1, tiles / 2);
@@ -352,6 +354,7 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
   a.wtail = u16(p.wcopy);
   a.targets = targets;
   a.xp = u16(p.xp);
+  a.xt = u16(p.xt);
   a.perm = reinterpret_cast<int32_t*>(ws + p.perm);
   a.tgt = reinterpret_cast<int32_t*>(ws + p.tgt);
   a.lse = f32(p.lse);
@@ -371,6 +374,7 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
   a.wfull = p.wfull;
   a.width = width;
   a.wpad = p.wpad;
+  a.ldxt = p.ldxt;
   a.ldw = p.copy_w ? p.wpad : width;
   a.ignore_index = ignore_index;
   a.grad_scale = grad_scale;

@@ -40,8 +40,6 @@ constexpr int kXThreads = 512;
 constexpr int kOperand = kXTile * kXStage;        // elements of one operand stage
 constexpr int kOperandB = kOperand * 2;           // 32 KiB
 constexpr int kXSmem = 4 * kOperandB;             // two stages of two operands
-constexpr int WM = 64, WN = 128;                  // a wave's block: 4 x 2 waves
-constexpr int MI = WM / 32, NI = WN / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -56,6 +54,16 @@ __device__ __forceinline__ void barrier() {
 // Chunk c (16 bytes) of a k-contiguous LDS row r sits at c ^ swz(r): any 16
 // consecutive rows of one chunk are spread over all banks.
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// A wave's block of the tile: MI x NI blocks of 32 x 32, 8 in all.
+template <int MI, int NI>
+struct Waves {
+  static constexpr int WM = 32 * MI, WN = 32 * NI, GN = kXTile / WN;
+  static_assert(MI * NI == 8 && (kXTile / WM) * GN == 8, "8 waves cover the tile");
+};
+// Transposing reads take twice the LDS time of plain ones (two 8-byte
+// accesses for one of 16), so an operand that needs them goes to the side a
+// wave has fewer fragments of.
 
 // One operand of the product: TR false, 256 rows of k-contiguous values (row
 // stride ld elements); TR true, k rows of 256 values along m.
@@ -113,12 +121,13 @@ __device__ __forceinline__ bf16x8_t frag(const uint16_t* stage, int base, int xk
 // overwrites the buffer of stage s - 1, whose last fragments were read in
 // phase 4 s - 1; its loads ride between the MFMAs of phases 4 s and 4 s + 1
 // and are waited for at the end of phase 4 s + 3, before their first use.
-template <bool TRA, bool TRB, typename FA, typename FB>
+template <bool TRA, bool TRB, int MI, int NI, typename FA, typename FB>
 __device__ __forceinline__ void product(char* smem, int nstage, FA&& abase, int64_t lda, int64_t acols, FB&& bbase,
                                         int64_t ldb, int64_t bcols, f32x16_t (&acc)[MI][NI]) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = wv >> 2, wm = wv >> 1, wn = wv & 1;
+  using G = Waves<MI, NI>;
+  const int grp = wv >> 2, wm = wv / G::GN, wn = wv % G::GN;
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -158,9 +167,9 @@ __device__ __forceinline__ void product(char* smem, int nstage, FA&& abase, int6
   for (int kk = 0; kk < 4; ++kk) xk[kk] = ((2 * kk + (lane >> 5)) ^ swz(lane & 31)) * 8;
   int ab[MI], bb[NI];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) ab[i] = frag_base<TRA>(wm * WM + i * 32, lane);
+  for (int i = 0; i < MI; ++i) ab[i] = frag_base<TRA>(wm * G::WM + i * 32, lane);
 #pragma unroll
-  for (int j = 0; j < NI; ++j) bb[j] = frag_base<TRB>(wn * WN + j * 32, lane);
+  for (int j = 0; j < NI; ++j) bb[j] = frag_base<TRB>(wn * G::WN + j * 32, lane);
   bf16x8_t fa[2][MI], fb[2][NI];
   auto read_half = [&](int s, int h) {
     const uint16_t* sa = reinterpret_cast<const uint16_t*>(smem + (s & 1) * 2 * kOperandB);
@@ -264,10 +273,11 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   const int64_t tok0 = (int64_t)tt * kXTile;
   if (tok0 >= count) return;
   const int64_t v0 = p.v0 + (int64_t)tv * kXTile;
+  constexpr int MI = 2, NI = 4, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
   f32x16_t acc[MI][NI];
   const uint16_t* const wt = w_row(a.w, a.wtail, a.wfull, a.ldw, v0);
   const uint16_t* const xt = a.xp + tok0 * a.wpad;
-  product<false, false>(
+  product<false, false, MI, NI>(
       smem, (int)(a.wpad / kXStage), [=](int s) { return wt + s * kXStage; }, a.ldw, 0,
       [=](int s) { return xt + s * kXStage; }, a.wpad, 0, acc);
 
@@ -374,18 +384,20 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     const XentArgs a, const XentPiece p, int ndw, int ndx, int nd) {
   __shared__ __attribute__((aligned(16))) char smem[kXSmem];
   const int count = a.sc->count;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int hi = lane >> 5;
-  f32x16_t acc[MI][NI];
   if ((int)blockIdx.x < ndw) {
+    constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
+    const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
+    f32x16_t acc[MI][NI];
     int tv, td;
-    block_order(xcd_job(blockIdx.x, ndw), ndw / nd, nd, tv, td);
+    block_order(xcd_job(blockIdx.x, ndw), nd, ndw / nd, td, tv);
     const int64_t d0 = (int64_t)td * kXTile, vl = (int64_t)tv * kXTile;  // word in the piece
-    const uint16_t* const xt = a.xp + d0;
+    const uint16_t* const xt = a.xt + d0 * a.ldxt;
     const uint16_t* const pt = a.prob + vl;
-    const int64_t ldx = a.wpad, ldp = p.cols;
-    product<true, true>(
-        smem, (count + kXStage - 1) / kXStage, [=](int s) { return xt + (int64_t)s * kXStage * ldx; }, ldx, ldx - d0,
+    const int64_t ldp = p.cols;
+    product<false, true, MI, NI>(
+        smem, (count + kXStage - 1) / kXStage, [=](int s) { return xt + s * kXStage; }, a.ldxt, 0,
         [=](int s) { return pt + (int64_t)s * kXStage * ldp; }, ldp, ldp - vl, acc);
     const float g = a.sc->gscale;
     WT* const dw = reinterpret_cast<WT*>(a.dw);
@@ -425,10 +437,13 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     }
     return;
   }
+  constexpr int MI = 2, NI = 4, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
+  const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
+  f32x16_t acc[MI][NI];
   const int job = xcd_job(blockIdx.x - ndw, ndx);
   const int per = ndx / p.splits, split = job / per;
   int tt, td;
-  block_order(job - split * per, per / nd, nd, tt, td);
+  block_order(job - split * per, nd, per / nd, td, tt);
   const int64_t tok0 = (int64_t)tt * kXTile, d0 = (int64_t)td * kXTile;
   if (tok0 >= count) return;
   // this split's stages of the piece
@@ -437,7 +452,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   const uint16_t* const pt = a.prob + tok0 * p.cols + (int64_t)s0 * kXStage;
   const uint16_t *const w = a.w + d0, *const tail = a.wtail + d0;
   const int64_t ldw = a.ldw, full = a.wfull, vs = p.v0 + (int64_t)s0 * kXStage;
-  product<true, false>(
+  product<true, false, MI, NI>(
       smem, s1 - s0, [=](int s) { return w_row(w, tail, full, ldw, vs + (int64_t)s * kXStage); }, ldw, a.wpad - d0,
       [=](int s) { return pt + (int64_t)s * kXStage; }, p.cols, 0, acc);
   float* const out = a.dxacc + (int64_t)split * a.npad * a.wpad;
@@ -553,6 +568,27 @@ __global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uin
     copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, vec, c, w_out + r * a.wpad);
 }
 
+// xt = xp transposed, 64 x 64 values a block.
+__global__ __launch_bounds__(256) void k_xent_transpose(const XentArgs a) {
+  __shared__ uint16_t t[64][72];
+  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  if (r0 >= a.sc->count) return;  // dw reads no further than the counted tokens' last stage
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    *reinterpret_cast<u32x4_t*>(&t[r + 32 * k][c]) =
+        *reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(a.xp + (r0 + r + 32 * k) * a.wpad + c0 + c));
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    u32x4_t q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      q[e] = (uint32_t)t[c + 2 * e][r + 32 * k] | (uint32_t)t[c + 2 * e + 1][r + 32 * k] << 16;
+    *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(a.xt + (c0 + r + 32 * k) * a.ldxt + r0 + c)) = q;
+  }
+}
+
 // lse and loss of each counted token from its tiles' statistics.
 __global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
   // 32 tokens a block; 8 threads share a token's tiles
@@ -658,6 +694,8 @@ hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w
   uint16_t* const w_out = const_cast<uint16_t*>(copy_w ? a.w : a.wtail);
   const int64_t wrows = copy_w ? a.rpad : a.rpad - a.wfull;
   hipLaunchKernelGGL(k_xent_gather, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
+  if (a.dw != nullptr)
+    hipLaunchKernelGGL(k_xent_transpose, dim3(a.npad / 64, a.wpad / 64), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -23,6 +23,7 @@ struct XentArgs {
   const uint16_t* wtail;             // rows [wfull, rows) padded to a whole tile, ldw
   const void* targets;
   uint16_t* xp;                      // counted tokens of x, npad x wpad, zero padded
+  uint16_t* xt;                      // xp transposed (for dw): width rounded up to a tile rows of ldxt
   int32_t* perm;                     // xp row -> token
   int32_t* tgt;                      // xp row -> target
   float* lse;                        // per xp row
@@ -35,7 +36,7 @@ struct XentArgs {
   float* token_loss;                 // per token, or nullptr
   uint16_t* dx;                      // n x width or nullptr
   void* dw;                          // rows x width or nullptr
-  int64_t n, npad, rows, rpad, wfull, width, wpad, ldw;
+  int64_t n, npad, rows, rpad, wfull, width, wpad, ldw, ldxt;
   int64_t ignore_index;
   float grad_scale;
   int32_t id_bits, mean, dw_dt, accumulate;
