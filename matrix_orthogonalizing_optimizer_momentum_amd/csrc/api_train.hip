@@ -148,8 +148,45 @@ int check_xent(const void* w, int64_t n, int64_t rows, int64_t width) {
   return MUONH_OK;
 }
 
+// Time of a launch in units of one operand stage: n1 jobs of c1, then n2 of c2,
+// each taken by the first compute unit that is free.
+int64_t makespan(int64_t n1, int64_t c1, int64_t n2, int64_t c2) {
+  const int64_t late = n1 % kXCus, early = kXCus - late;  // units that end the first kind a round later
+  int64_t te = n1 / kXCus * c1, tl = te + c1, end = late ? tl : te;
+  while (n2 > 0) {
+    if (te <= tl || late == 0) {
+      n2 -= early;
+      end = std::max(end, te += c2);
+    } else {
+      n2 -= late;
+      end = std::max(end, tl += c2);
+    }
+  }
+  return end;
+}
+
+// Estimated time of both gradients with pieces of `tiles` tiles and dx in
+// `splits` parts (also where only one is asked for, so that dx is the same
+// sum of parts with and without dw).  Beside its stages a job costs the time of a few more:
+// measured 3 us a tile of P, 8 us a tile of dw or dx, where a stage takes 1.6.
+int64_t xent_cost(int64_t ntok, int64_t nvoc, int64_t wpad, int64_t tiles, int64_t splits) {
+  constexpr int64_t kProbExtra = 2, kGradExtra = 5;
+  const int64_t nd = up(wpad, kXTile) / kXTile, per = kXTile / kXStage;
+  int64_t t = 0;
+  auto piece = [&](int64_t k) {
+    const int64_t cw = ntok * per + kGradExtra, cx = (k * per + splits - 1) / splits + kGradExtra;
+    const int64_t nw = k * nd, nx = ntok * nd * splits;
+    return makespan(ntok * k, wpad / kXStage + kProbExtra, 0, 0) +
+           (cx > cw ? makespan(nx, cx, nw, cw) : makespan(nw, cw, nx, cx));
+  };
+  t += nvoc / tiles * piece(tiles);
+  if (nvoc % tiles) t += piece(nvoc % tiles);
+  return t;
+}
+
 // Layout for a piece of `cols` words (0: no gradient).
-XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t cols) {
+XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t cols,
+                     int64_t splits) {
   XentPlan p{};
   // w's rows are an operand as they stand when they are whole stages on a
   // 16-byte grid; else the call works on a padded copy
@@ -178,29 +215,42 @@ XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool
   p.area = take(std::max<int64_t>(8 * (p.rpad / kXTile) * p.npad, 2 * p.npad * cols));
   if (cols > 0) {
     p.pieces = (p.rpad + cols - 1) / cols;
-    // dx jobs about as deep as dw's (the tokens), so that a launch's jobs are alike
-    p.splits = dx ? std::min<int64_t>(std::max<int64_t>(1, (cols + p.npad / 2) / p.npad), 8) : 1;
+    p.splits = splits;
     if (dx) p.dxacc = take(4 * p.splits * p.npad * p.wpad);
   }
   p.bytes = at;
   return p;
 }
 
-// The largest piece whose layout fits `limit`; pieces are balanced.
+// The piece and split, among those whose layout fits `limit`, that fill the
+// rounds of the chip best (by xent_cost): pieces of the largest size down to
+// half of it, smaller ones only where the limit asks for them.
 int xent_plan(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t limit, XentPlan& p) {
   const int64_t npad = up(std::max<int64_t>(n, 1), kXTile), rpad = up(rows, kXTile);
   if (!dx && !dw) {
-    p = xent_layout(w, n, rows, width, false, false, 0);
+    p = xent_layout(w, n, rows, width, false, false, 0, 1);
     return p.bytes <= limit ? MUONH_OK : MUONH_ENOMEM;
   }
-  int64_t tiles = std::max<int64_t>(1, std::min(rpad, kXentPieceBytes / (2 * npad)) / kXTile);
-  for (;;) {
-    const int64_t pieces = (rpad / kXTile + tiles - 1) / tiles;
-    tiles = (rpad / kXTile + pieces - 1) / pieces;
-    p = xent_layout(w, n, rows, width, dx, dw, tiles * kXTile);
-    if (p.bytes <= limit) return MUONH_OK;
-    if (tiles == 1) return MUONH_ENOMEM;
-    tiles = std::max<int64_t>(1, tiles / 2);
+  const int64_t ntok = npad / kXTile, nvoc = rpad / kXTile, wpad = up(width, kXStage);
+  int64_t top = std::max<int64_t>(1, std::min(rpad, kXentPieceBytes / (2 * npad)) / kXTile);
+  for (;; top = std::max<int64_t>(1, top / 2)) {
+    int64_t best = 0, best_tiles = 0, best_splits = 0;
+    const int64_t step = std::max<int64_t>(1, top / 32);
+    for (int64_t tiles = top; tiles > top / 2; tiles -= step)
+      for (int64_t splits = 1; splits <= kXMaxSplits && splits <= tiles; splits *= 2) {
+        if (xent_layout(w, n, rows, width, dx, dw, tiles * kXTile, splits).bytes > limit) continue;
+        const int64_t t = xent_cost(ntok, nvoc, wpad, tiles, splits);
+        if (best_tiles == 0 || t < best) {
+          best = t;
+          best_tiles = tiles;
+          best_splits = splits;
+        }
+      }
+    if (best_tiles) {
+      p = xent_layout(w, n, rows, width, dx, dw, best_tiles * kXTile, best_splits);
+      return MUONH_OK;
+    }
+    if (top == 1) return MUONH_ENOMEM;
   }
 }
 
@@ -394,7 +444,8 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
   MUONH_TRY_HIP(launch_xent_loss(a, s));
   if (!dx && !dw) return MUONH_OK;
   for (int64_t v0 = 0; v0 < p.rpad; v0 += p.cols) {
-    const XentPiece pc{v0, std::min(p.cols, p.rpad - v0), (int32_t)p.splits, v0 == 0 ? 1 : 0};
+    XentPiece pc{v0, std::min(p.cols, p.rpad - v0), (int32_t)p.splits, v0 == 0 ? 1 : 0, 0};
+    pc.dx_first = pc.cols / pc.splits > p.npad ? 1 : 0;  // the longer jobs first
     const double share = (double)pc.cols / (double)p.rpad;
     {
       ProfScope pf(s, PC_XPROB, mac * share, 0);

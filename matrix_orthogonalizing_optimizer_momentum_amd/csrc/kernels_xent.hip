@@ -24,6 +24,8 @@
 // through gfx950's transposing LDS read, so neither P, x nor w is ever
 // transposed in memory.  The side a lane holds four consecutive values of (m)
 // is the one the result's rows run along: words for P, width for dx and dw.
+#include <type_traits>
+
 #include "common.h"
 #include "xent.h"
 
@@ -263,121 +265,321 @@ __device__ __forceinline__ const uint16_t* w_row(const uint16_t* w, const uint16
 // ---------------------------------------------------------------------------
 // logits of a 256-word x 256-token tile: statistics (first pass) or P
 // ---------------------------------------------------------------------------
+// Persistent: workgroup b takes every gridDim / 8-th job of its XCD's run.  The
+// operand stages of all its tiles form one stream: while the last stage of a
+// tile is multiplied, the first one of the next is already on its way, and the
+// epilogues run with those loads in flight.  (One tile a workgroup: 8.6 us of
+// launch, first load and epilogue beside 17 us of products at width 768.)
 template <bool STATS>
 __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_logits(
-    const XentArgs a, const XentPiece p, int ntok, int nvoc) {
-  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
-  int tt, tv;
-  block_order(xcd_job(blockIdx.x, ntok * nvoc), ntok, nvoc, tt, tv);
-  const int count = a.sc->count;
-  const int64_t tok0 = (int64_t)tt * kXTile;
-  if (tok0 >= count) return;
-  const int64_t v0 = p.v0 + (int64_t)tv * kXTile;
+    const XentArgs a, const XentPiece p, int nvoc) {
   constexpr int MI = 2, NI = 4, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
-  f32x16_t acc[MI][NI];
-  const uint16_t* const wt = w_row(a.w, a.wtail, a.wfull, a.ldw, v0);
-  const uint16_t* const xt = a.xp + tok0 * a.wpad;
-  product<false, false, MI, NI>(
-      smem, (int)(a.wpad / kXStage), [=](int s) { return wt + s * kXStage; }, a.ldw, 0,
-      [=](int s) { return xt + s * kXStage; }, a.wpad, 0, acc);
+  // operand stages, then (STATS) the maximum and sum of each token per row of
+  // waves.  One array: with the latter in an array of its own, which the
+  // compiler placed first, the kernel ran 10% longer.
+  __shared__ __attribute__((aligned(16))) char smem[kXSmem + (STATS ? 4 * kXTile * (int)sizeof(float2) : 0)];
+  float2* const st = reinterpret_cast<float2*>(smem + kXSmem);
+  const int count = a.sc->count;
+  const int ntok = (count + kXTile - 1) / kXTile;
+  const int njobs = ntok * nvoc;
+  const int xcd = blockIdx.x % 8, step = gridDim.x / 8;
+  const int q = njobs / 8, rem = njobs % 8;
+  const int end = xcd * q + min(xcd, rem) + q + (xcd < rem ? 1 : 0);
+  int job = xcd * q + min(xcd, rem) + (int)(blockIdx.x / 8);
+  if (job >= end) return;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const int hi = lane >> 5;
-  const int64_t vw = v0 + wm * WM;                   // the wave's first word
-  const int words = (int)min<int64_t>(WM, a.rows - vw);  // of them real (may be <= 0)
-  // word of acc[i][.][v], counted from vw
-  auto word = [&](int i, int v) { return i * 32 + 8 * (v >> 2) + 4 * hi + (v & 3); };
-  if constexpr (STATS) {
-    float2* const st = reinterpret_cast<float2*>(smem);  // [4][256]
-    __syncthreads();
+  const int tid = threadIdx.x, lane = tid & 63, hi = lane >> 5;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wv >> 2, wm = wv / Waves<MI, NI>::GN, wn = wv % Waves<MI, NI>::GN;
+  const int nstage = (int)(a.wpad / kXStage);
+  const int64_t ldw = a.ldw, ldx = a.wpad, full = a.wfull;
+  const uint16_t *const w = a.w, *const tail = a.wtail, *const xp = a.xp;
+  uint32_t voff, rstride;
+  {
+    Operand<false> o;
+    o.init(wv & 3, lane, grp == 0 ? ldw : ldx, 0);
+    voff = o.voff;
+    rstride = __builtin_amdgcn_readfirstlane(o.rstride);
+  }
+  auto origin = [&](int j, int64_t& tok0, int64_t& v0) {
+    int tt, tv;
+    block_order(j, ntok, nvoc, tt, tv);
+    tok0 = (int64_t)tt * kXTile;
+    v0 = p.v0 + (int64_t)tv * kXTile;
+  };
+  // this wave's operand of a tile: words (waves 0-3) or tokens (4-7)
+  auto source = [&](int64_t tok0, int64_t v0) -> const char* {
+    return reinterpret_cast<const char*>(grp == 0 ? w_row(w, tail, full, ldw, v0) : xp + tok0 * ldx);
+  };
+  const int half = grp * kOperandB + (wv & 3) * 1024;
+  // run r of a stage; src moves on to the next one
+  auto load_run = [&](const char*& src, int buf, int r) {
+    __builtin_amdgcn_global_load_lds(
+        (MUONH_GLOBAL void*)(gmem(src) + voff),
+        (__attribute__((address_space(3))) void*)(smem + buf * 2 * kOperandB + half + 4 * r * 1024), 16, 0, 0);
+    src += rstride;
+  };
+  auto load_stage = [&](const char* src, int buf) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int tl = wn * WN + j * 32 + (lane & 31);
-      if (words < WM) {
+    for (int r = 0; r < 8; ++r) load_run(src, buf, r);
+  };
+  int xk[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) xk[kk] = ((2 * kk + hi) ^ swz(lane & 31)) * 8;
+  int ab[MI], bb[NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) ab[i] = frag_base<false>(wm * WM + i * 32, lane);
+#pragma unroll
+  for (int j = 0; j < NI; ++j) bb[j] = frag_base<false>(wn * WN + j * 32, lane);
+  f32x16_t acc[MI][NI];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  };
+  bf16x8_t fa[2][MI], fb[2][NI];
+  auto read_half = [&](int buf, int h) {
+    const uint16_t* sa = reinterpret_cast<const uint16_t*>(smem + buf * 2 * kOperandB);
+    const uint16_t* sb = sa + kOperand;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[k][i] = frag<false>(sa, ab[i], xk[2 * h + k], 0);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[k][j] = frag<false>(sb, bb[j], xk[2 * h + k], 0);
+    }
+  };
+  // a half stage's 16 MFMAs, LOAD: with this wave's loads of the next stage
+  // (from src, into buffer buf) in between
+  auto mma_half = [&](auto load_c, const char* src, int buf) {
+    constexpr bool LOAD = decltype(load_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int t = 0; t < 2 * MI * NI; ++t) {
+      const int k = t / (MI * NI), i = (t / NI) % MI, j = t % NI;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[k][i], fb[k][j], acc[i][j], 0, 0, 0);
+      if (t & 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (LOAD) load_run(src, buf, t / 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // What becomes of a finished tile.
+  auto epilogue = [&](int64_t tok0, int64_t v0) {
+    const int64_t vw = v0 + wm * WM;                       // the wave's first word
+    const int words = (int)max<int64_t>(0, min<int64_t>(WM, a.rows - vw));  // of them real
+    // word of acc[i][.][v], counted from the lane's first one, vw + 4 hi
+    auto word = [](int i, int v) { return i * 32 + 8 * (v >> 2) + (v & 3); };
+    // the same count for a word t of the vocabulary; far outside for others
+    auto rel = [&](int t) {
+      const int64_t r = (int64_t)t - vw;
+      return t >= 0 && r >= 0 && r < WM ? (int)r - 4 * hi : -64;
+    };
+    if (words < WM) {  // the last tile: words that are none get no weight
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int v = 0; v < 16; ++v)
-            if (word(i, v) >= words) acc[i][j][v] = -INFINITY;
-      }
-      float m = acc[0][j][0];
+            if (word(i, v) >= words - 4 * hi) acc[i][j][v] = -INFINITY;
+    }
+    if constexpr (STATS) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
-      m = fmaxf(m, __shfl_xor(m, 32, 64));
-      const float mb = m == -INFINITY ? 0.f : m * kLog2e;  // nothing finite: the sum is 0
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -mb));
-      s += __shfl_xor(s, 32, 64);
-      if (hi == 0) st[wm * kXTile + tl] = make_float2(m, s);
-      // the target's logit, where this wave holds it
-      const int64_t ci = tok0 + tl;
-      const int64_t t = ci < count ? (int64_t)a.tgt[ci] - vw : -1;
-      const bool have = t >= 0 && t < WM && ((t >> 2) & 1) == hi;
-      if (__ballot(have)) {
-        float l = 0.f;
+      for (int j = 0; j < NI; ++j) {
+        const int tl = wn * WN + j * 32 + (lane & 31);
+        float m = acc[0][j][0];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) l = word(i, v) == t ? acc[i][j][v] : l;
-        if (have) a.tlogit[ci] = l;
+          for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const float mb = m == -INFINITY ? 0.f : m * kLog2e;  // nothing finite: the sum is 0
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -mb));
+        s += __shfl_xor(s, 32, 64);
+        if (hi == 0) st[wm * kXTile + tl] = make_float2(m, s);
+        // the target's logit, where this wave holds it
+        const int64_t ci = tok0 + tl;
+        const int t = rel(ci < count ? a.tgt[ci] : -1);
+        if (__ballot(t != -64)) {
+          float l = 0.f;
+          bool have = false;
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              l = word(i, v) == t ? acc[i][j][v] : l;
+              have |= word(i, v) == t;
+            }
+          if (have) a.tlogit[ci] = l;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
+        const bool in = ci < count;
+        const float lb = in ? a.lse[ci] * kLog2e : 0.f;
+        const int t = rel(in ? a.tgt[ci] : -1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
+            acc[i][j][v] = in ? x : 0.f;
+          }
+        // - 1 at the target, where this wave holds any token's
+        if (__ballot(t != -64)) {
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] -= word(i, v) == t ? 1.f : 0.f;
+        }
+        uint16_t* const row = a.prob + ci * p.cols + (vw - p.v0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int pq = 0; pq < 2; ++pq) {
+            const f32x16_t e = acc[i][j];
+            const int o = 8 * pq;
+            // lanes l and l + 32 trade groups: each then holds 8 consecutive words
+            const uint32_t w0 = pack_bf16x2(e[o], e[o + 1]), w1 = pack_bf16x2(e[o + 2], e[o + 3]);
+            const uint32_t w2 = pack_bf16x2(e[o + 4], e[o + 5]), w3 = pack_bf16x2(e[o + 6], e[o + 7]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w0, w2, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w1, w3, false, false);
+            const u32x4_t pk = {s0[0], s1[0], s0[1], s1[1]};
+            *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(row + i * 32 + 16 * pq + 8 * hi)) = pk;
+          }
       }
     }
-    __syncthreads();
-    if (tid < kXTile) {
-      float m = st[tid].x;
+  };
+  // Joins the four rows of waves of a tile, a barrier after its epilogue: one
+  // token a thread of waves 4-7.
+  auto join = [&](int64_t tok0, int64_t v0) {
+    if constexpr (STATS) {
+      const int t = tid & (kXTile - 1);
+      float m = st[t].x;
 #pragma unroll
-      for (int k = 1; k < 4; ++k) m = fmaxf(m, st[k * kXTile + tid].x);
+      for (int k = 1; k < 4; ++k) m = fmaxf(m, st[k * kXTile + t].x);
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 q = st[k * kXTile + tid];
-        s += q.x == -INFINITY ? q.y : q.y * __builtin_amdgcn_exp2f((q.x - m) * kLog2e);
+        const float2 r = st[k * kXTile + t];
+        s += r.x == -INFINITY ? r.y : r.y * __builtin_amdgcn_exp2f((r.x - m) * kLog2e);
       }
-      a.stats[(v0 / kXTile) * a.npad + tok0 + tid] = make_float2(m, s);
+      a.stats[(v0 / kXTile) * a.npad + tok0 + t] = make_float2(m, s);
     }
+  };
+
+  int64_t tok0, v0, ntok0 = 0, nv0 = 0;
+  origin(job, tok0, v0);
+  const char* src = source(tok0, v0);
+  // After its last tile a workgroup loads that tile's first stage once more,
+  // to no use, which keeps the loop free of branches around the loads.
+  const char* nsrc;
+  const std::true_type load{};
+  const std::false_type no_load{};
+  clear();
+  load_stage(src, 0);
+  wait_loads();
+  barrier();
+  int buf = 0;
+  // phases of a stage as in product(); a barrier ends each
+  if (grp == 0) {
+    for (;;) {
+      const int next = job + step;
+      nsrc = src;
+      if (next < end) {
+        origin(next, ntok0, nv0);
+        nsrc = source(ntok0, nv0);
+      }
+      for (int s = 0; s < nstage; ++s) {
+        read_half(buf, 0);
+        wait_lds();
+        barrier();
+        mma_half(load, s + 1 < nstage ? src + (s + 1) * (kXStage * 2) : nsrc, buf ^ 1);
+        barrier();
+        read_half(buf, 1);
+        wait_lds();
+        barrier();
+        mma_half(no_load, src, 0);
+        wait_loads();
+        barrier();
+        buf ^= 1;
+      }
+      epilogue(tok0, v0);
+      if (next >= end) break;
+      clear();
+      job = next;
+      tok0 = ntok0;
+      v0 = nv0;
+      src = nsrc;
+    }
+    if constexpr (STATS) __syncthreads();
   } else {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
-      const bool in = ci < count;
-      const float lb = in ? a.lse[ci] * kLog2e : 0.f;
-      const int64_t t = in ? (int64_t)a.tgt[ci] - vw : -1;
-      uint16_t* const row = a.prob + ci * p.cols + (vw - p.v0);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int pq = 0; pq < 2; ++pq) {
-          float e[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int v = 4 * (2 * pq + h) + k, wd = word(i, v);
-              float q = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
-              q = wd == t ? q - 1.f : q;
-              e[h][k] = in && wd < words ? q : 0.f;
-            }
-          // lanes l and l + 32 trade groups: each then holds 8 consecutive words
-          const uint32_t w0 = pack_bf16x2(e[0][0], e[0][1]), w1 = pack_bf16x2(e[0][2], e[0][3]);
-          const uint32_t w2 = pack_bf16x2(e[1][0], e[1][1]), w3 = pack_bf16x2(e[1][2], e[1][3]);
-          const auto s0 = __builtin_amdgcn_permlane32_swap(w0, w2, false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(w1, w3, false, false);
-          const u32x4_t pk = {s0[0], s1[0], s0[1], s1[1]};
-          *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(row + i * 32 + 16 * pq + 8 * hi)) = pk;
+    int64_t ptok0 = -1, pv0 = 0;  // the tile before, whose last MFMAs and epilogue fall into this one's first phase
+    for (;;) {
+      const int next = job + step;
+      nsrc = src;
+      if (next < end) {
+        origin(next, ntok0, nv0);
+        nsrc = source(ntok0, nv0);
+      }
+      for (int s = 0; s < nstage; ++s) {
+        const char* const ld = s + 1 < nstage ? src + (s + 1) * (kXStage * 2) : nsrc;
+        if (s > 0 || ptok0 >= 0) mma_half(load, ld, buf ^ 1);
+        else load_stage(ld, buf ^ 1);
+        if (s == 0 && ptok0 >= 0) {
+          epilogue(ptok0, pv0);
+          clear();
         }
+        barrier();
+        if (s == 0 && ptok0 >= 0) join(ptok0, pv0);
+        __builtin_amdgcn_sched_barrier(0);
+        read_half(buf, 0);
+        wait_lds();
+        barrier();
+        mma_half(no_load, src, 0);
+        barrier();
+        read_half(buf, 1);
+        wait_lds();
+        wait_loads();
+        barrier();
+        buf ^= 1;
+      }
+      ptok0 = tok0;
+      pv0 = v0;
+      if (next >= end) break;
+      job = next;
+      tok0 = ntok0;
+      v0 = nv0;
+      src = nsrc;
+    }
+    mma_half(no_load, src, 0);
+    epilogue(ptok0, pv0);
+    if constexpr (STATS) {
+      __syncthreads();
+      join(ptok0, pv0);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// gradients of one piece: jobs [0, ndw) are dw tiles (256 of width x 256
-// words, depth = tokens), the rest dx tiles (256 of width x 256 tokens, depth
-// = one split of the piece's words)
+// gradients of one piece: ndw jobs are dw tiles (256 of width x 256 words,
+// depth = tokens), ndx dx tiles (256 of width x 256 tokens, depth = one split
+// of the piece's words); the kind with the longer jobs starts
 // ---------------------------------------------------------------------------
 template <typename WT>
 __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_grad(
@@ -386,12 +588,14 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   const int count = a.sc->count;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int hi = lane >> 5;
-  if ((int)blockIdx.x < ndw) {
+  const bool is_dw = p.dx_first ? (int)blockIdx.x >= ndx : (int)blockIdx.x < ndw;
+  const int job0 = (int)blockIdx.x - (is_dw == (p.dx_first != 0) ? (is_dw ? ndx : ndw) : 0);
+  if (is_dw) {
     constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
     const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
     f32x16_t acc[MI][NI];
     int tv, td;
-    block_order(xcd_job(blockIdx.x, ndw), nd, ndw / nd, td, tv);
+    block_order(xcd_job(job0, ndw), nd, ndw / nd, td, tv);
     const int64_t d0 = (int64_t)td * kXTile, vl = (int64_t)tv * kXTile;  // word in the piece
     const uint16_t* const xt = a.xt + d0 * a.ldxt;
     const uint16_t* const pt = a.prob + vl;
@@ -440,7 +644,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   constexpr int MI = 2, NI = 4, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
   const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
   f32x16_t acc[MI][NI];
-  const int job = xcd_job(blockIdx.x - ndw, ndx);
+  const int job = xcd_job(job0, ndx);
   const int per = ndx / p.splits, split = job / per;
   int tt, td;
   block_order(job - split * per, nd, per / nd, td, tt);
@@ -699,10 +903,17 @@ hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w
   return hipGetLastError();
 }
 
+// Persistent workgroups of the logits kernels: one a CU, whole rounds over the
+// XCDs.
+static int logit_blocks(const XentArgs& a, int nvoc) {
+  const int64_t jobs = a.npad / kXTile * nvoc;
+  return (int)(jobs < kXCus ? (jobs + 7) / 8 * 8 : kXCus);
+}
+
 hipError_t launch_xent_stats(const XentArgs& a, hipStream_t s) {
-  const int ntok = (int)(a.npad / kXTile), nvoc = (int)(a.rpad / kXTile);
-  const XentPiece p{0, a.rpad, 1, 1};
-  hipLaunchKernelGGL((k_xent_logits<true>), dim3(ntok * nvoc), dim3(kXThreads), 0, s, a, p, ntok, nvoc);
+  const int nvoc = (int)(a.rpad / kXTile);
+  const XentPiece p{0, a.rpad, 1, 1, 0};
+  hipLaunchKernelGGL((k_xent_logits<true>), dim3(logit_blocks(a, nvoc)), dim3(kXThreads), 0, s, a, p, nvoc);
   return hipGetLastError();
 }
 
@@ -713,8 +924,8 @@ hipError_t launch_xent_loss(const XentArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_xent_prob(const XentArgs& a, const XentPiece& p, hipStream_t s) {
-  const int ntok = (int)(a.npad / kXTile), nvoc = (int)(p.cols / kXTile);
-  hipLaunchKernelGGL((k_xent_logits<false>), dim3(ntok * nvoc), dim3(kXThreads), 0, s, a, p, ntok, nvoc);
+  const int nvoc = (int)(p.cols / kXTile);
+  hipLaunchKernelGGL((k_xent_logits<false>), dim3(logit_blocks(a, nvoc)), dim3(kXThreads), 0, s, a, p, nvoc);
   return hipGetLastError();
 }
 

@@ -8,6 +8,8 @@ namespace muonh {
 
 constexpr int kXTile = 256;          // output tile side of the products
 constexpr int kXStage = 64;          // depth of one operand stage
+constexpr int kXCus = 256;            // compute units, a multiple of the 8 XCDs
+constexpr int kXMaxSplits = 8;
 constexpr int64_t kXMaxWidth = 65536;
 
 // Device scalars of one call.
@@ -48,6 +50,7 @@ struct XentPiece {
   int64_t v0, cols;
   int32_t splits;                    // parts of cols that dx is summed over separately
   int32_t first;                     // the first piece: dxacc is written, not added to
+  int32_t dx_first;                  // order of the jobs of one launch
 };
 
 hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w_in, hipStream_t s);
