@@ -98,7 +98,8 @@ int check_embedding(const void* ids, int id_bits, int64_t n, int64_t rows, int64
 
 // Scratch of the embedding gradient.
 struct EmbedPlan {
-  int bits, passes, tile, blocks;
+  bool solo;
+  int need, bits, passes, tile, blocks, run;
   int64_t key[2], pos[2], hist, part, bytes;
 };
 
@@ -106,6 +107,8 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
   EmbedPlan p{};
   int need = 1;  // bits of the largest key, rows itself (the ignored tokens)
   while (((int64_t)1 << need) <= rows) ++need;
+  p.need = need;
+  p.solo = n <= kSoloTokens;
   p.passes = (need + kSortBits - 1) / kSortBits;
   p.bits = (need + p.passes - 1) / p.passes;
   // tiles of at least 1024 tokens (256 a wave), at most kSortMaxBlocks of them:
@@ -123,7 +126,11 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
     p.pos[k] = take(4 * n);
   }
   p.hist = take(4 * ((int64_t)p.blocks << p.bits));
-  p.part = take(8 * ((n + kRun - 1) / kRun) * width);
+  // Pieces as long as leave 16 waves a CU (a wave takes 512 columns of a piece):
+  // long ones save partial rows, short ones fill the chip at few tokens.
+  p.run = kRunMax;
+  while (p.run > kRunMin && (n + p.run - 1) / p.run * ((width + 511) / 512) < 4096) p.run /= 2;
+  p.part = take(8 * ((n + p.run - 1) / p.run) * width);
   p.bytes = std::max<int64_t>(at, 256);
   return p;
 }
@@ -341,8 +348,26 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
   char* const ws = reinterpret_cast<char*>(workspace);
   auto u32 = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   int cur = 0;
-  if (n > 0) {
-    ProfScope pf(s, PC_EMBSORT, 0, (double)n * (id_bits / 8 + 16.0 * p.passes - 8.0));
+  ZeroSlice z{static_cast<uint16_t*>(dtable), rows * width * dtype_size(dtable_dtype) / 2, 0, 0};
+  if (n == 0) {
+    z.count = accumulate ? 0 : 1;
+    MUONH_TRY_HIP(launch_zero(z, s));
+    return MUONH_OK;
+  }
+  if (p.solo) {
+    ProfScope pf(s, PC_EMBSORT, 0, (double)n * (id_bits / 8 + 8.0) + (accumulate ? 0.0 : 2.0 * (double)z.halves));
+    SortPass sp{};
+    sp.ids = ids;
+    sp.key_out = u32(p.key[0]);
+    sp.pos_out = u32(p.pos[0]);
+    sp.n = n;
+    sp.rows = (uint32_t)rows;
+    sp.id_bits = id_bits;
+    sp.bits = p.need;
+    z.count = accumulate ? 0 : 1;
+    MUONH_TRY_HIP(launch_sort_solo(sp, z, s));
+  } else {
+    ProfScope pf(s, PC_EMBSORT, 0, (double)n * (id_bits / 8 + 16.0 * p.passes - 8.0) + (accumulate ? 0.0 : 2.0 * (double)z.halves));
     for (int k = 0; k < p.passes; ++k) {
       SortPass sp{};
       sp.ids = k == 0 ? ids : nullptr;
@@ -358,14 +383,18 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
       sp.bits = p.bits;
       sp.tile = p.tile;
       sp.blocks = p.blocks;
-      MUONH_TRY_HIP(launch_sort_pass(sp, s));
+      ZeroSlice z0 = z, z1 = z;
+      z0.count = z1.count = accumulate ? 0 : 2 * p.passes;
+      z0.index = 2 * k;
+      z1.index = 2 * k + 1;
+      MUONH_TRY_HIP(launch_sort_pass(sp, z0, z1, s));
       cur ^= 1;
     }
   }
   ProfScope pf(s, PC_EMBGRAD, 0,
-               (double)n * width * dtype_size(dout_dtype) + (double)rows * width * dtype_size(dtable_dtype));
+               (double)n * (double)width * (double)(dtype_size(dout_dtype) + dtype_size(dtable_dtype)));
   const EmbedGradArgs a{u32(p.key[cur]), u32(p.pos[cur]), dout, dtable, reinterpret_cast<float*>(ws + p.part),
-                        n, rows, width, scale, accumulate};
+                        n, rows, width, scale, accumulate, p.run};
   MUONH_TRY_HIP(launch_embedding_grad(internal_dtype(dout_dtype), internal_dtype(dtable_dtype), a, s));
   return MUONH_OK;
 }

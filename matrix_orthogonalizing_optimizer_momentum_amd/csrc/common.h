@@ -101,6 +101,10 @@ template <> struct Raw8<bf16_t> {
   __device__ __forceinline__ void load(const bf16_t* p, int64_t i) {
     q = *reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(p + i));
   }
+  // non-temporal: for data that the kernel reads once and nothing reads again soon
+  __device__ __forceinline__ void load_once(const bf16_t* p, int64_t i) {
+    q = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(p + i)));
+  }
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -114,6 +118,10 @@ template <> struct Raw8<float> {
   __device__ __forceinline__ void load(const float* p, int64_t i) {
     a = *reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i));
     b = *reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i + 4));
+  }
+  __device__ __forceinline__ void load_once(const float* p, int64_t i) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i)));
+    b = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i + 4)));
   }
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = a[0]; v[1] = a[1]; v[2] = a[2]; v[3] = a[3];

@@ -10,7 +10,19 @@ constexpr int64_t kEmbMaxWidth = (int64_t)1 << 18;
 constexpr int kSortThreads = 256;
 constexpr int kSortBits = 11;      // digit bits of one sort pass, at most
 constexpr int kSortMaxBlocks = 64;
-constexpr int kRun = 32;           // sorted tokens per piece of the gradient
+constexpr int kSoloThreads = 1024;  // the sort in one workgroup:
+constexpr int kSoloItems = 8;       // tokens per thread (8192 tokens on 50257 x 768: 37 us, by passes 52; 16384: 61 and 56)
+constexpr int kSoloBits = 9;        // digit bits of one of its passes
+constexpr int64_t kSoloTokens = kSoloThreads * kSoloItems;
+constexpr int kRunMin = 8, kRunMax = 32;  // sorted tokens per piece of the gradient
+
+// A share of the table's gradient that a launch clears: slice `index` of
+// `count` equal ones (count 0: nothing).  p is aligned to 2 bytes.
+struct ZeroSlice {
+  uint16_t* p;
+  int64_t halves;           // of the whole table, in units of 2 bytes
+  int32_t index, count;
+};
 
 // One stable counting pass of the token sort.
 struct SortPass {
@@ -43,10 +55,15 @@ struct EmbedGradArgs {
   int64_t n, rows, width;
   float scale;
   int32_t accumulate;
+  int32_t run;              // tokens per piece, a multiple of 8
 };
 
 hipError_t launch_embedding(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t s);
-hipError_t launch_sort_pass(const SortPass& p, hipStream_t s);
+// count and scatter of one pass, with one slice of the clearing each
+hipError_t launch_sort_pass(const SortPass& p, const ZeroSlice& count_z, const ZeroSlice& scatter_z, hipStream_t s);
+// up to kSoloTokens tokens, all passes; p.bits is the key's width
+hipError_t launch_sort_solo(const SortPass& p, const ZeroSlice& z, hipStream_t s);
+hipError_t launch_zero(const ZeroSlice& z, hipStream_t s);
 hipError_t launch_embedding_grad(int g_dt, int out_dt, const EmbedGradArgs& a, hipStream_t s);
 
 }  // namespace muonh

@@ -5,11 +5,16 @@
 //
 // The gradient sorts the tokens by id (stable: tokens of one id stay in batch
 // order), so that every row of the table is summed in a fixed order without
-// atomics.  Sorted tokens are cut into pieces of kRun; a piece sums its runs of
-// equal ids in fp32 and writes the rows whose run lies inside it.  Runs that
+// atomics.  Sorted tokens are cut into pieces; a piece sums its runs of equal
+// ids in fp32 and writes the rows whose run lies inside it.  Runs that
 // cross pieces (frequent tokens) leave one partial row per piece, which
-// k_embed_join adds in order.  All of it is bound by HBM: dout is read once and
-// the table's gradient is written once, the rows without a token included.
+// k_embed_join adds in order.
+//
+// All of it is bound by HBM: dout is read once, and the whole of the table's
+// gradient is written.  The sort is a chain of short steps that leaves the
+// chip idle, so its launches carry the clearing of the table in further
+// workgroups: the zeros cost no time of their own, at the price of writing the
+// rows that have tokens twice (8192 tokens on 50257 x 768 fp32: 25 of 154 MB).
 #include "common.h"
 #include "embed.h"
 
@@ -76,6 +81,28 @@ __global__ __launch_bounds__(kEmbThreads) void k_embedding(const EmbedArgs a, ui
 }
 
 // ---------------------------------------------------------------------------
+// clearing, as further workgroups (first_block on) of another launch
+// ---------------------------------------------------------------------------
+template <int NT>
+__device__ void zero_slice(const ZeroSlice& z, int64_t block, int64_t blocks) {
+  const int64_t head = min<int64_t>(((16 - (uintptr_t)z.p % 16) % 16) / 2, z.halves);
+  const int64_t vecs = (z.halves - head) / 8, tail0 = head + vecs * 8;
+  if (z.index == 0 && block == 0) {  // what lies before and after the 16-byte grid
+    if (threadIdx.x < head) gmem(z.p)[threadIdx.x] = 0;
+    if (threadIdx.x >= 64 && tail0 + (threadIdx.x - 64) < z.halves && threadIdx.x < 72)
+      gmem(z.p)[tail0 + (threadIdx.x - 64)] = 0;
+  }
+  const int64_t lo = vecs * z.index / z.count, n = vecs * (z.index + 1) / z.count - lo;
+  // a contiguous run a block
+  const int64_t b0 = n * block / blocks, b1 = n * (block + 1) / blocks;
+  MUONH_GLOBAL u32x4_t* const p = reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(z.p + head)) + lo;
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  for (int64_t i = b0 + threadIdx.x; i < b1; i += NT) p[i] = zero;
+}
+
+__global__ __launch_bounds__(256) void k_zero(const ZeroSlice z) { zero_slice<256>(z, blockIdx.x, gridDim.x); }
+
+// ---------------------------------------------------------------------------
 // stable sort of the tokens by id: counting passes over digits of the id, the
 // lowest first.  A block owns a contiguous tile of tokens, a wave of it a
 // contiguous quarter.
@@ -86,8 +113,29 @@ __device__ __forceinline__ uint32_t pass_key(const SortPass& p, int64_t i) {
   return p.ids != nullptr ? token_key(p.ids, p.id_bits, i, p.rows) : gmem(p.key_in)[i];
 }
 
-__global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortPass p) {
+// The next place of digit d in a wave's table, for each lane with `in`: a
+// token's rank among the wave's equal digits is the number of lower lanes that
+// hold the same one, and the lowest of them moves the place on.
+__device__ __forceinline__ uint32_t take_place(uint32_t* next, uint32_t d, int bits, bool in) {
+  const int lane = threadIdx.x & 63;
+  uint64_t same = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t m = __ballot((d >> b) & 1);
+    same &= ((d >> b) & 1) ? m : ~m;
+  }
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  const int lead = in ? __ffsll((unsigned long long)same) - 1 : lane;
+  uint32_t first = 0;
+  if (in && rank == 0) first = atomicAdd(&next[d], (uint32_t)__popcll(same));
+  return __shfl(first, lead, 64) + rank;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortPass p, const ZeroSlice z) {
   __shared__ uint32_t cnt[1 << kSortBits];
+  if ((int)blockIdx.x >= p.blocks) {
+    zero_slice<kSortThreads>(z, blockIdx.x - p.blocks, gridDim.x - p.blocks);
+    return;
+  }
   const uint32_t bins = 1u << p.bits;
   for (uint32_t d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
   __syncthreads();
@@ -98,10 +146,14 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortPass p) {
   for (uint32_t d = threadIdx.x; d < bins; d += kSortThreads) gmem(p.hist)[(int64_t)blockIdx.x * bins + d] = cnt[d];
 }
 
-__global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p) {
+__global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p, const ZeroSlice z) {
   // next free place of each digit, one table per wave
   __shared__ uint32_t next[kSortWaves][1 << kSortBits];
   __shared__ uint32_t sums[kSortWaves];
+  if ((int)blockIdx.x >= p.blocks) {
+    zero_slice<kSortThreads>(z, blockIdx.x - p.blocks, gridDim.x - p.blocks);
+    return;
+  }
   const uint32_t bins = 1u << p.bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t lo = (int64_t)blockIdx.x * p.tile;
@@ -123,10 +175,18 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p)
     tot[k] = before[k] = 0;
     if (k < per && owner) {
       const uint32_t d = tid * per + k;
-      for (int b = 0; b < p.blocks; ++b) {
-        const uint32_t c = gmem(p.hist)[(int64_t)b * bins + d];
-        tot[k] += c;
-        if (b < (int)blockIdx.x) before[k] += c;
+      // a batch of blocks' counts in flight at a time
+      constexpr int B = 16;
+      for (int b0 = 0; b0 < p.blocks; b0 += B) {
+        uint32_t c[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) c[u] = gmem(p.hist)[(int64_t)min(b0 + u, p.blocks - 1) * bins + d];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          const uint32_t v = b0 + u < p.blocks ? c[u] : 0u;
+          tot[k] += v;
+          before[k] += b0 + u < (int)blockIdx.x ? v : 0u;
+        }
       }
       mine += tot[k];
     }
@@ -156,41 +216,111 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p)
     }
   }
   __syncthreads();
-  // 64 tokens at a time, in order: a token's rank among the wave's equal
-  // digits is the number of lower lanes that hold the same one.
+  // 64 tokens at a time, in order
   for (int64_t i0 = wlo; i0 < whi; i0 += 64) {
     const int64_t i = i0 + lane;
     const bool in = i < whi;
     const uint32_t key = in ? pass_key(p, i) : 0u;
     const uint32_t pos = in ? (p.ids != nullptr ? (uint32_t)i : gmem(p.pos_in)[i]) : 0u;
-    const uint32_t d = (key >> p.shift) & (bins - 1);
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < p.bits; ++b) {
-      const uint64_t m = __ballot((d >> b) & 1);
-      same &= ((d >> b) & 1) ? m : ~m;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    const int lead = in ? __ffsll((unsigned long long)same) - 1 : lane;
-    uint32_t first = 0;
-    if (in && rank == 0) first = atomicAdd(&next[wave][d], (uint32_t)__popcll(same));
-    first = __shfl(first, lead, 64);
+    const uint32_t at = take_place(next[wave], (key >> p.shift) & (bins - 1), p.bits, in);
     if (in) {
-      gmem(p.key_out)[first + rank] = key;
-      gmem(p.pos_out)[first + rank] = pos;
+      gmem(p.key_out)[at] = key;
+      gmem(p.pos_out)[at] = pos;
     }
   }
+}
+
+// All passes in one workgroup, the tokens in LDS between them: 16 waves, wave
+// w owns a contiguous run of tokens.  At 8192 tokens it takes less than the
+// launches of the passes above.
+__global__ __launch_bounds__(kSoloThreads) void k_sort_solo(const SortPass p, const ZeroSlice z) {
+  constexpr int NW = kSoloThreads / 64, BINS = 1 << kSoloBits;
+  __shared__ uint32_t skey[kSoloTokens];
+  __shared__ uint16_t spos[kSoloTokens];
+  __shared__ uint32_t next[NW][BINS];
+  __shared__ uint32_t sums[NW];
+  if (blockIdx.x > 0) {
+    zero_slice<kSoloThreads>(z, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = (int)p.n;
+  const int rounds = (n + kSoloThreads - 1) / kSoloThreads;
+  const int i0 = wave * rounds * 64 + lane;  // this lane's tokens: i0 + 64 r
+  uint32_t key[kSoloItems], pos[kSoloItems], at[kSoloItems];
+#pragma unroll
+  for (int r = 0; r < kSoloItems; ++r) {
+    const int i = i0 + 64 * r;
+    pos[r] = i;
+    key[r] = r < rounds && i < n ? token_key(p.ids, p.id_bits, i, p.rows) : 0u;
+  }
+  for (int shift = 0; shift < p.bits; shift += kSoloBits) {
+    const int bits = min(kSoloBits, p.bits - shift);
+    for (int d = tid; d < NW * BINS; d += kSoloThreads) next[d / BINS][d % BINS] = 0;
+    __syncthreads();
+    // each token's place among its wave's equal digits; next ends as their counts
+#pragma unroll
+    for (int r = 0; r < kSoloItems; ++r)
+      if (r < rounds) at[r] = take_place(next[wave], (key[r] >> shift) & (BINS - 1), bits, i0 + 64 * r < n);
+    __syncthreads();
+    // digit tid: where it starts, then where each wave's share of it starts
+    uint32_t tot = 0;
+    if (tid < BINS) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) tot += next[w][tid];
+    }
+    uint32_t incl = tot;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    if (tid < BINS) {
+      uint32_t base = incl - tot;
+      for (int w = 0; w < wave; ++w) base += sums[w];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const uint32_t c = next[w][tid];
+        next[w][tid] = base;
+        base += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSoloItems; ++r)
+      if (r < rounds && i0 + 64 * r < n) {
+        const uint32_t to = next[wave][(key[r] >> shift) & (BINS - 1)] + at[r];
+        skey[to] = key[r];
+        spos[to] = (uint16_t)pos[r];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSoloItems; ++r)
+      if (r < rounds && i0 + 64 * r < n) {
+        key[r] = skey[i0 + 64 * r];
+        pos[r] = spos[i0 + 64 * r];
+      }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < kSoloItems; ++r)
+    if (r < rounds && i0 + 64 * r < n) {
+      gmem(p.key_out)[i0 + 64 * r] = key[r];
+      gmem(p.pos_out)[i0 + 64 * r] = pos[r];
+    }
 }
 
 // ---------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------
 constexpr int kEgThreads = 256;
-constexpr int kZeroRows = 64;  // rows per block of the pass over rows without tokens
 
 template <typename GT, int V> struct Chunk;
 template <typename GT> struct Chunk<GT, 8> {
   Raw8<GT> r;
-  __device__ __forceinline__ void load(const GT* p, int64_t i) { r.load(p, i); }
+  __device__ __forceinline__ void load(const GT* p, int64_t i) { r.load_once(p, i); }
   __device__ __forceinline__ void add(float (&acc)[8]) const {
     float v[8];
     r.unpack(v);
@@ -230,54 +360,24 @@ __device__ __forceinline__ void add_part(const float* p, int64_t i, float (&acc)
 }
 __device__ __forceinline__ void add_part(const float* p, int64_t i, float (&acc)[1]) { acc[0] += gmem(p)[i]; }
 
-// Writes zeros to the rows [row0, row0 + kZeroRows) that hold no token.
-template <typename OT, int V>
-__device__ void zero_rows(const EmbedGradArgs& a, int64_t row0, uint32_t cpr) {
-  __shared__ uint32_t absent[kZeroRows];
-  if (threadIdx.x < kZeroRows) {
-    const int64_t v = row0 + threadIdx.x;
-    // first sorted place with a key >= v
-    int64_t lo = 0, hi = a.n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (gmem(a.key)[mid] < v) lo = mid + 1;
-      else hi = mid;
-    }
-    absent[threadIdx.x] = v < a.rows && (lo >= a.n || gmem(a.key)[lo] != v);
-  }
-  __syncthreads();
-  OT* const o = reinterpret_cast<OT*>(a.dtable);
-  for (uint32_t x = threadIdx.x; x < kZeroRows * cpr; x += kEgThreads) {
-    const uint32_t r = x / cpr;
-    if (!absent[r]) continue;
-    const int64_t at = (row0 + r) * a.width + (int64_t)(x - r * cpr) * V;
-    if constexpr (V == 8) {
-      const float z[8] = {};
-      store8(o, at, z);
-    } else {
-      St<OT>::st(o, at, 0.f);
-    }
-  }
-}
-
-// Blocks [0, nsum): sums; the others: rows without tokens.  One launch, so
-// that the zeros are written while the sums wait for their gathered rows.
+// One wave: one piece of sorted tokens, 64 chunks of V columns.  The keys and
+// places are the same for all lanes (scalar loads, scalar branches), and the
+// rows of 8 tokens are in flight at a time.
 template <typename GT, typename OT, int V>
-__global__ __launch_bounds__(kEgThreads) void k_embed_grad(const EmbedGradArgs a, uint32_t cpr, int nsum) {
-  if ((int)blockIdx.x >= nsum) {
-    zero_rows<OT, V>(a, (int64_t)((int)blockIdx.x - nsum) * kZeroRows, cpr);
-    return;
-  }
-  const int64_t g = (int64_t)blockIdx.x * kEgThreads + threadIdx.x;
-  const int64_t piece = g / cpr;
-  const int64_t col = (g - piece * cpr) * V;
-  const int64_t s = piece * kRun, e = min(a.n, s + kRun);
-  if (s >= a.n) return;
+__global__ __launch_bounds__(kEgThreads) void k_embed_grad(const EmbedGradArgs a, uint32_t cpr, uint32_t groups) {
+  typedef __attribute__((address_space(4))) const uint32_t ro_t;
+  ro_t* const keys = reinterpret_cast<ro_t*>(reinterpret_cast<uintptr_t>(a.key));
+  ro_t* const places = reinterpret_cast<ro_t*>(reinterpret_cast<uintptr_t>(a.pos));
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kEgThreads / 64) + (threadIdx.x >> 6));
+  const uint32_t piece = wave / groups, chunk = (wave - piece * groups) * 64 + (threadIdx.x & 63);
+  const int64_t s = (int64_t)piece * a.run, e = min(a.n, s + a.run);
+  if (s >= a.n || chunk >= cpr) return;
+  const int64_t col = (int64_t)chunk * V;
   const GT* const dout = reinterpret_cast<const GT*>(a.dout);
-  float* const head = a.part + 2 * piece * a.width;
+  float* const head = a.part + 2 * (int64_t)piece * a.width;
   float* const tail = head + a.width;
-  uint32_t cur = gmem(a.key)[s];
-  bool before = s > 0 && gmem(a.key)[s - 1] == cur;
+  uint32_t cur = keys[s];
+  bool before = s > 0 && keys[s - 1] == cur;
   float acc[V] = {};
   auto flush = [&](bool onward) {
     if (cur >= a.rows) return;
@@ -285,63 +385,90 @@ __global__ __launch_bounds__(kEgThreads) void k_embed_grad(const EmbedGradArgs a
     else if (onward) put_part(tail, col, acc);
     else put_row<OT>(a, cur, col, acc);
   };
+  auto take = [&](uint32_t k, const Chunk<GT, V>& c) {
+    if (k != cur) {
+      flush(false);
+      cur = k;
+      before = false;
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] = 0.f;
+    }
+    c.add(acc);
+  };
   constexpr int U = 8;
-  for (int64_t i0 = s; i0 < e; i0 += U) {
+  int64_t i = s;
+  for (; i + U <= e; i += U) {
     uint32_t k[U];
     Chunk<GT, V> c[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = min(i0 + u, e - 1);
-      k[u] = gmem(a.key)[i];
-      c[u].load(dout, (int64_t)gmem(a.pos)[i] * a.width + col);
+      k[u] = keys[i + u];
+      c[u].load(dout, (int64_t)places[i + u] * a.width + col);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u >= e) break;
-      if (k[u] != cur) {
-        flush(false);
-        cur = k[u];
-        before = false;
-#pragma unroll
-        for (int x = 0; x < V; ++x) acc[x] = 0.f;
-      }
-      c[u].add(acc);
-    }
+    for (int u = 0; u < U; ++u) take(k[u], c[u]);
   }
-  flush(e < a.n && gmem(a.key)[e] == cur);
+  for (; i < e; ++i) {
+    Chunk<GT, V> c;
+    c.load(dout, (int64_t)places[i] * a.width + col);
+    take(keys[i], c);
+  }
+  flush(e < a.n && keys[e] == cur);
 }
 
 // Rows whose run crosses pieces: the piece where the run starts adds its tail
-// and the heads of the pieces that follow.
+// and the heads of the pieces that follow.  A block takes kJoinCols chunks of
+// columns; its kJoinParts groups of threads each add a contiguous share of the
+// heads (a frequent token has hundreds), and the shares are added in order.
+constexpr int kJoinCols = 64, kJoinParts = kEgThreads / kJoinCols;
 template <typename OT, int V>
 __global__ __launch_bounds__(kEgThreads) void k_embed_join(const EmbedGradArgs a, uint32_t cpr) {
   const int64_t piece = blockIdx.x;
-  const int64_t s = piece * kRun, e = s + kRun;
+  const int64_t s = piece * a.run, e = s + a.run;
   if (e >= a.n) return;
   const uint32_t k = gmem(a.key)[e - 1];
   if (k >= a.rows || gmem(a.key)[e] != k) return;
   if (s > 0 && gmem(a.key)[s - 1] == k) return;  // the run started in an earlier piece
-  const int64_t pieces = (a.n + kRun - 1) / kRun;
-  // pieces piece + 1 .. last begin with this key
-  __shared__ int64_t last_s;
-  if (threadIdx.x < 64) {
-    int64_t q = piece + 1;
-    for (;;) {
-      const int64_t c = q + threadIdx.x;
-      const bool same = c < pieces && gmem(a.key)[c * kRun] == k;
-      const int run = __popcll(__ballot(same));  // keys are sorted: a prefix of the lanes
-      q += run;
-      if (run < 64) break;
-    }
-    if (threadIdx.x == 0) last_s = q;
+  const int64_t pieces = (a.n + a.run - 1) / a.run;
+  // pieces piece + 1 .. end - 1 begin with this key; every wave finds end itself
+  const int lane = threadIdx.x & 63;
+  int64_t end = piece + 1;
+  for (;;) {
+    const int64_t c = end + lane;
+    const bool same = c < pieces && gmem(a.key)[c * a.run] == k;
+    const int run = __popcll(__ballot(same));  // keys are sorted: a prefix of the lanes
+    end += run;
+    if (run < 64) break;
   }
+  __shared__ float share[kJoinParts][kJoinCols][V];
+  const int cl = threadIdx.x % kJoinCols, part = threadIdx.x / kJoinCols;
+  const uint32_t chunk = blockIdx.y * kJoinCols + cl;
+  const bool in = chunk < cpr;
+  const int64_t col = (int64_t)(in ? chunk : 0) * V;
+  const int64_t heads = end - (piece + 1);
+  const int64_t q0 = piece + 1 + heads * part / kJoinParts, q1 = piece + 1 + heads * (part + 1) / kJoinParts;
+  float acc[V] = {};
+  if (part == 0) add_part(a.part + (2 * piece + 1) * a.width, col, acc);
+  constexpr int U = 8;
+  int64_t q = q0;
+  for (; q + U <= q1; q += U) {
+    float v[U][V] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) add_part(a.part + 2 * (q + u) * a.width, col, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] += v[u][x];
+  }
+  for (; q < q1; ++q) add_part(a.part + 2 * q * a.width, col, acc);
+#pragma unroll
+  for (int x = 0; x < V; ++x) share[part][cl][x] = acc[x];
   __syncthreads();
-  const int64_t end = last_s;
-  for (uint32_t c = threadIdx.x; c < cpr; c += kEgThreads) {
-    const int64_t col = (int64_t)c * V;
-    float acc[V] = {};
-    add_part(a.part + (2 * piece + 1) * a.width, col, acc);
-    for (int64_t q = piece + 1; q < end; ++q) add_part(a.part + 2 * q * a.width, col, acc);
+  if (part == 0 && in) {
+#pragma unroll
+    for (int r = 1; r < kJoinParts; ++r)
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] += share[r][cl][x];
     put_row<OT>(a, k, col, acc);
   }
 }
@@ -373,24 +500,45 @@ hipError_t launch_embedding(int table_dt, int out_dt, const EmbedArgs& a, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_sort_pass(const SortPass& p, hipStream_t s) {
-  hipLaunchKernelGGL(k_sort_count, dim3(p.blocks), dim3(kSortThreads), 0, s, p);
-  hipLaunchKernelGGL(k_sort_scatter, dim3(p.blocks), dim3(kSortThreads), 0, s, p);
+// Workgroups that clear a slice: 64 KiB each of 256 threads, at most 8 a CU.
+static int zero_blocks(const ZeroSlice& z) {
+  if (z.count == 0 || z.halves == 0) return 0;
+  const int64_t b = (z.halves / z.count * 2 + 65535) / 65536;
+  return (int)(b < 1 ? 1 : b > 2048 ? 2048 : b);
+}
+
+hipError_t launch_sort_pass(const SortPass& p, const ZeroSlice& count_z, const ZeroSlice& scatter_z, hipStream_t s) {
+  hipLaunchKernelGGL(k_sort_count, dim3(p.blocks + zero_blocks(count_z)), dim3(kSortThreads), 0, s, p, count_z);
+  hipLaunchKernelGGL(k_sort_scatter, dim3(p.blocks + zero_blocks(scatter_z)), dim3(kSortThreads), 0, s, p, scatter_z);
+  return hipGetLastError();
+}
+
+hipError_t launch_sort_solo(const SortPass& p, const ZeroSlice& z, hipStream_t s) {
+  const int zb = zero_blocks(z);  // one workgroup a CU fits beside the sort's LDS
+  hipLaunchKernelGGL(k_sort_solo, dim3(1 + (zb > 255 ? 255 : zb)), dim3(kSoloThreads), 0, s, p, z);
+  return hipGetLastError();
+}
+
+hipError_t launch_zero(const ZeroSlice& z, hipStream_t s) {
+  const int zb = zero_blocks(z);
+  if (zb > 0) hipLaunchKernelGGL(k_zero, dim3(zb), dim3(256), 0, s, z);
   return hipGetLastError();
 }
 
 hipError_t launch_embedding_grad(int g_dt, int out_dt, const EmbedGradArgs& a, hipStream_t s) {
   const bool v8 = vec8(a.width, a.dout, a.dtable);
   const uint32_t cpr = (uint32_t)(v8 ? a.width / 8 : a.width);
-  const int64_t pieces = (a.n + kRun - 1) / kRun;
-  const int64_t nsum = (pieces * cpr + kEgThreads - 1) / kEgThreads;
-  const int64_t nzero = a.accumulate ? 0 : (a.rows + kZeroRows - 1) / kZeroRows;
-  if (nsum + nzero > INT32_MAX) return hipErrorInvalidValue;
-#define MUONH_EG(GT, OT, V)                                                                                     \
-  do {                                                                                                          \
-    if (nsum + nzero > 0)                                                                                       \
-      hipLaunchKernelGGL((k_embed_grad<GT, OT, V>), dim3(nsum + nzero), dim3(kEgThreads), 0, s, a, cpr, (int)nsum); \
-    if (pieces > 1) hipLaunchKernelGGL((k_embed_join<OT, V>), dim3(pieces), dim3(kEgThreads), 0, s, a, cpr);    \
+  const int64_t pieces = (a.n + a.run - 1) / a.run;
+  const uint32_t groups = (cpr + 63) / 64;
+  const int64_t nsum = (pieces * groups + kEgThreads / 64 - 1) / (kEgThreads / 64);
+  if (nsum <= 0) return hipSuccess;
+  if (nsum > INT32_MAX || pieces > INT32_MAX) return hipErrorInvalidValue;
+#define MUONH_EG(GT, OT, V)                                                                              \
+  do {                                                                                                   \
+    hipLaunchKernelGGL((k_embed_grad<GT, OT, V>), dim3(nsum), dim3(kEgThreads), 0, s, a, cpr, groups);   \
+    if (pieces > 1)                                                                                      \
+      hipLaunchKernelGGL((k_embed_join<OT, V>), dim3(pieces, (cpr + kJoinCols - 1) / kJoinCols),         \
+                         dim3(kEgThreads), 0, s, a, cpr);                                                \
   } while (0)
 #define MUONH_EG_V(GT, OT)       \
   do {                           \
