@@ -371,8 +371,7 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
  *   out     device, n x width, MUONH_F32 or MUONH_BF16 (one rounding)
  *   n       0 .. 2^31 - 1;  rows  1 .. 2^31 - 2;  width  1 .. 2^18 (larger:
  *           MUONH_ENOTIMPL);  scale  finite
- * Rows whose width is a multiple of 8, on 16-byte aligned buffers, take
- * 16-byte accesses; others are read element by element.
+ * Buffers need no more than their elements' alignment.
  */
 int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t width, const void* ids, int id_bits,
                     int64_t n, float scale, void* out, int out_dtype, void* stream);

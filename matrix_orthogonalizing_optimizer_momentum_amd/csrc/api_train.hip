@@ -130,7 +130,7 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
   // long ones save partial rows, short ones fill the chip at few tokens.
   p.run = kRunMax;
   while (p.run > kRunMin && (n + p.run - 1) / p.run * ((width + 511) / 512) < 4096) p.run /= 2;
-  p.part = take(8 * ((n + p.run - 1) / p.run) * width);
+  p.part = take(8 * ((n + p.run - 1) / p.run) * up(width, 8));
   p.bytes = std::max<int64_t>(at, 256);
   return p;
 }

@@ -91,6 +91,24 @@ __device__ __forceinline__ void load8(const float* p, int64_t i, float (&v)[8]) 
   v[0] = a[0]; v[1] = a[1]; v[2] = a[2]; v[3] = a[3];
   v[4] = b[0]; v[5] = b[1]; v[6] = b[2]; v[7] = b[3];
 }
+// The same at any element alignment: gfx950's global accesses of 16 bytes need
+// no more than the element's own.
+typedef u32x4_t __attribute__((aligned(2))) u32x4_u;
+typedef f32x4_t __attribute__((aligned(4))) f32x4_u;
+__device__ __forceinline__ void load8_any(const bf16_t* p, int64_t i, float (&v)[8]) {
+  const u32x4_t q = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p + i));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(q[k] << 16);
+    v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8_any(const float* p, int64_t i, float (&v)[8]) {
+  const f32x4_t a = *reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i));
+  const f32x4_t b = *reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4));
+  v[0] = a[0]; v[1] = a[1]; v[2] = a[2]; v[3] = a[3];
+  v[4] = b[0]; v[5] = b[1]; v[6] = b[2]; v[7] = b[3];
+}
 // 8 consecutive elements held in their storage form until unpacked.  A batch
 // of them can be in flight before any value is used; a conversion right next
 // to its load (above all inside a branch) makes the compiler wait for that
@@ -101,9 +119,13 @@ template <> struct Raw8<bf16_t> {
   __device__ __forceinline__ void load(const bf16_t* p, int64_t i) {
     q = *reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(p + i));
   }
-  // non-temporal: for data that the kernel reads once and nothing reads again soon
+  // any element alignment
+  __device__ __forceinline__ void load_any(const bf16_t* p, int64_t i) {
+    q = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p + i));
+  }
+  // and non-temporal: for data that the kernel reads once and nothing reads again soon
   __device__ __forceinline__ void load_once(const bf16_t* p, int64_t i) {
-    q = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(p + i)));
+    q = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p + i)));
   }
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
 #pragma unroll
@@ -119,9 +141,13 @@ template <> struct Raw8<float> {
     a = *reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i));
     b = *reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i + 4));
   }
+  __device__ __forceinline__ void load_any(const float* p, int64_t i) {
+    a = *reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i));
+    b = *reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4));
+  }
   __device__ __forceinline__ void load_once(const float* p, int64_t i) {
-    a = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i)));
-    b = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + i + 4)));
+    a = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i)));
+    b = __builtin_nontemporal_load(reinterpret_cast<const MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4)));
   }
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = a[0]; v[1] = a[1]; v[2] = a[2]; v[3] = a[3];
@@ -160,6 +186,18 @@ __device__ __forceinline__ void store8(float* p, int64_t i, const float (&v)[8])
   const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
   *reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(p + i)) = a;
   *reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(p + i + 4)) = b;
+}
+
+__device__ __forceinline__ void store8_any(bf16_t* p, int64_t i, const float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+  *reinterpret_cast<MUONH_GLOBAL u32x4_u*>(gmem(p + i)) = w;
+}
+__device__ __forceinline__ void store8_any(float* p, int64_t i, const float (&v)[8]) {
+  const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+  *reinterpret_cast<MUONH_GLOBAL f32x4_u*>(gmem(p + i)) = a;
+  *reinterpret_cast<MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4)) = b;
 }
 
 // Store one element of run-time dtype.

@@ -22,6 +22,21 @@ namespace muonh {
 
 namespace {
 
+// A row is cut into chunks of V columns: 8, at any alignment, or 1 for rows
+// shorter than that.  The last chunk of a row that is no whole number of
+// them is moved back to end with the row, and leaves its first `skip` columns
+// to the chunk before.
+template <int V>
+__device__ __forceinline__ int64_t chunk_col(uint32_t chunk, int64_t width, int& skip) {
+  if constexpr (V == 1) {
+    skip = 0;
+    return chunk;
+  }
+  const int64_t c = (int64_t)chunk * V, last = width - V;
+  skip = (int)(c > last ? c - last : 0);
+  return c - skip;
+}
+
 __device__ __forceinline__ uint32_t token_key(const void* ids, int id_bits, int64_t i, uint32_t rows) {
   if (id_bits == 32) {
     const uint32_t v = gmem(reinterpret_cast<const uint32_t*>(ids))[i];
@@ -34,7 +49,7 @@ __device__ __forceinline__ uint32_t token_key(const void* ids, int id_bits, int6
 // ---------------------------------------------------------------------------
 // lookup
 // ---------------------------------------------------------------------------
-// Flat over the V-element chunks of the output; a block's first row and chunk
+// Flat over the V-column chunks of the output; a block's first row and chunk
 // come from one 64-bit division, a thread's from a 32-bit one.
 constexpr int kEmbThreads = 256;
 constexpr int kEmbPer = 4;  // chunks per thread, all loads in flight together
@@ -47,20 +62,22 @@ __global__ __launch_bounds__(kEmbThreads) void k_embedding(const EmbedArgs a, ui
   const TT* const table = reinterpret_cast<const TT*>(a.table);
   OT* const out = reinterpret_cast<OT*>(a.out);
   int64_t row[kEmbPer];
-  uint32_t col[kEmbPer], key[kEmbPer];
+  int64_t col[kEmbPer];
+  uint32_t key[kEmbPer];
+  int skip[kEmbPer];
 #pragma unroll
   for (int k = 0; k < kEmbPer; ++k) {
     const uint32_t x = off0 + threadIdx.x + k * kEmbThreads;
     const uint32_t q = x / cpr;
     row[k] = row0 + q;
-    col[k] = (x - q * cpr) * V;
+    col[k] = chunk_col<V>(x - q * cpr, a.width, skip[k]);
     key[k] = row[k] < a.n ? token_key(a.ids, a.id_bits, row[k], (uint32_t)a.rows) : (uint32_t)a.rows;
   }
   if constexpr (V == 8) {
     Raw8<TT> r[kEmbPer];
 #pragma unroll
     for (int k = 0; k < kEmbPer; ++k)
-      if (key[k] < a.rows) r[k].load(table, (int64_t)key[k] * a.width + col[k]);
+      if (key[k] < a.rows) r[k].load_any(table, (int64_t)key[k] * a.width + col[k]);
 #pragma unroll
     for (int k = 0; k < kEmbPer; ++k) {
       if (row[k] >= a.n) continue;
@@ -68,7 +85,14 @@ __global__ __launch_bounds__(kEmbThreads) void k_embedding(const EmbedArgs a, ui
       r[k].unpack(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = key[k] < a.rows ? a.scale * v[e] : 0.f;
-      store8(out, row[k] * a.width + col[k], v);
+      const int64_t at = row[k] * a.width + col[k];
+      if (skip[k] == 0) {
+        store8_any(out, at, v);
+      } else {
+#pragma unroll
+        for (int e = 1; e < 8; ++e)
+          if (e >= skip[k]) St<OT>::st(out, at + e, v[e]);
+      }
     }
   } else {
 #pragma unroll
@@ -335,17 +359,25 @@ template <typename GT> struct Chunk<GT, 1> {
 };
 
 template <typename OT>
-__device__ __forceinline__ void put_row(const EmbedGradArgs& a, uint32_t key, int64_t col, const float (&acc)[8]) {
+__device__ __forceinline__ void put_row(const EmbedGradArgs& a, uint32_t key, int64_t col, int skip,
+                                        const float (&acc)[8]) {
   OT* const o = reinterpret_cast<OT*>(a.dtable);
   const int64_t at = (int64_t)key * a.width + col;
   float v[8];
-  if (a.accumulate) load8(o, at, v);
+  if (a.accumulate) load8_any(o, at, v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = a.accumulate ? fmaf(a.scale, acc[e], v[e]) : a.scale * acc[e];
-  store8(o, at, v);
+  if (skip == 0) {
+    store8_any(o, at, v);
+  } else {
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+      if (e >= skip) St<OT>::st(o, at + e, v[e]);
+  }
 }
 template <typename OT>
-__device__ __forceinline__ void put_row(const EmbedGradArgs& a, uint32_t key, int64_t col, const float (&acc)[1]) {
+__device__ __forceinline__ void put_row(const EmbedGradArgs& a, uint32_t key, int64_t col, int skip,
+                                        const float (&acc)[1]) {
   OT* const o = reinterpret_cast<OT*>(a.dtable);
   const int64_t at = (int64_t)key * a.width + col;
   St<OT>::st(o, at, a.accumulate ? fmaf(a.scale, acc[0], St<OT>::ld(o, at)) : a.scale * acc[0]);
@@ -372,18 +404,20 @@ __global__ __launch_bounds__(kEgThreads) void k_embed_grad(const EmbedGradArgs a
   const uint32_t piece = wave / groups, chunk = (wave - piece * groups) * 64 + (threadIdx.x & 63);
   const int64_t s = (int64_t)piece * a.run, e = min(a.n, s + a.run);
   if (s >= a.n || chunk >= cpr) return;
-  const int64_t col = (int64_t)chunk * V;
+  int skip;
+  const int64_t col = chunk_col<V>(chunk, a.width, skip), at = (int64_t)chunk * V;
   const GT* const dout = reinterpret_cast<const GT*>(a.dout);
-  float* const head = a.part + 2 * (int64_t)piece * a.width;
-  float* const tail = head + a.width;
+  const int64_t pitch = (int64_t)cpr * V;  // of a partial row
+  float* const head = a.part + 2 * (int64_t)piece * pitch;
+  float* const tail = head + pitch;
   uint32_t cur = keys[s];
   bool before = s > 0 && keys[s - 1] == cur;
   float acc[V] = {};
   auto flush = [&](bool onward) {
     if (cur >= a.rows) return;
-    if (before) put_part(head, col, acc);
-    else if (onward) put_part(tail, col, acc);
-    else put_row<OT>(a, cur, col, acc);
+    if (before) put_part(head, at, acc);
+    else if (onward) put_part(tail, at, acc);
+    else put_row<OT>(a, cur, col, skip, acc);
   };
   auto take = [&](uint32_t k, const Chunk<GT, V>& c) {
     if (k != cur) {
@@ -444,23 +478,25 @@ __global__ __launch_bounds__(kEgThreads) void k_embed_join(const EmbedGradArgs a
   const int cl = threadIdx.x % kJoinCols, part = threadIdx.x / kJoinCols;
   const uint32_t chunk = blockIdx.y * kJoinCols + cl;
   const bool in = chunk < cpr;
-  const int64_t col = (int64_t)(in ? chunk : 0) * V;
+  int skip;
+  const int64_t col = chunk_col<V>(in ? chunk : 0, a.width, skip), at = (int64_t)(in ? chunk : 0) * V;
+  const int64_t pitch = (int64_t)cpr * V;
   const int64_t heads = end - (piece + 1);
   const int64_t q0 = piece + 1 + heads * part / kJoinParts, q1 = piece + 1 + heads * (part + 1) / kJoinParts;
   float acc[V] = {};
-  if (part == 0) add_part(a.part + (2 * piece + 1) * a.width, col, acc);
+  if (part == 0) add_part(a.part + (2 * piece + 1) * pitch, at, acc);
   constexpr int U = 8;
   int64_t q = q0;
   for (; q + U <= q1; q += U) {
     float v[U][V] = {};
 #pragma unroll
-    for (int u = 0; u < U; ++u) add_part(a.part + 2 * (q + u) * a.width, col, v[u]);
+    for (int u = 0; u < U; ++u) add_part(a.part + 2 * (q + u) * pitch, at, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int x = 0; x < V; ++x) acc[x] += v[u][x];
   }
-  for (; q < q1; ++q) add_part(a.part + 2 * q * a.width, col, acc);
+  for (; q < q1; ++q) add_part(a.part + 2 * q * pitch, at, acc);
 #pragma unroll
   for (int x = 0; x < V; ++x) share[part][cl][x] = acc[x];
   __syncthreads();
@@ -469,20 +505,15 @@ __global__ __launch_bounds__(kEgThreads) void k_embed_join(const EmbedGradArgs a
     for (int r = 1; r < kJoinParts; ++r)
 #pragma unroll
       for (int x = 0; x < V; ++x) acc[x] += share[r][cl][x];
-    put_row<OT>(a, k, col, acc);
+    put_row<OT>(a, k, col, skip, acc);
   }
 }
 
 }  // namespace
 
-// 16-byte accesses need rows of whole 8-element chunks on a 16-byte grid.
-static bool vec8(int64_t width, const void* p, const void* q) {
-  return width % 8 == 0 && ((uintptr_t)p | (uintptr_t)q) % 16 == 0;
-}
-
 hipError_t launch_embedding(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t s) {
-  const bool v8 = vec8(a.width, a.table, a.out);
-  const uint32_t cpr = (uint32_t)(v8 ? a.width / 8 : a.width);
+  const bool v8 = a.width >= 8;
+  const uint32_t cpr = (uint32_t)(v8 ? (a.width + 7) / 8 : a.width);
   const int64_t chunks = a.n * cpr, per = kEmbThreads * kEmbPer;
   const int64_t blocks = (chunks + per - 1) / per;
   if (blocks <= 0) return hipSuccess;
@@ -526,8 +557,8 @@ hipError_t launch_zero(const ZeroSlice& z, hipStream_t s) {
 }
 
 hipError_t launch_embedding_grad(int g_dt, int out_dt, const EmbedGradArgs& a, hipStream_t s) {
-  const bool v8 = vec8(a.width, a.dout, a.dtable);
-  const uint32_t cpr = (uint32_t)(v8 ? a.width / 8 : a.width);
+  const bool v8 = a.width >= 8;
+  const uint32_t cpr = (uint32_t)(v8 ? (a.width + 7) / 8 : a.width);
   const int64_t pieces = (a.n + a.run - 1) / a.run;
   const uint32_t groups = (cpr + 63) / 64;
   const int64_t nsum = (pieces * groups + kEgThreads / 64 - 1) / (kEgThreads / 64);
