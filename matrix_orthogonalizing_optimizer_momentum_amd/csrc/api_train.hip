@@ -322,7 +322,8 @@ int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t wi
   if (n == 0) return MUONH_OK;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   ProfScope pf(s, PC_EMB, 0, (double)n * (double)width * (double)(dtype_size(table_dtype) + dtype_size(out_dtype)));
-  const EmbedArgs a{table, ids, out, n, rows, width, scale, id_bits};
+  const EmbedArgs a{table, ids, out, n, rows, width, scale, id_bits,
+                    n * width * dtype_size(out_dtype) > kEmbOnceBytes ? 1 : 0};
   MUONH_TRY_HIP(launch_embedding(internal_dtype(table_dtype), internal_dtype(out_dtype), a, s));
   return MUONH_OK;
 }

@@ -200,6 +200,20 @@ __device__ __forceinline__ void store8_any(float* p, int64_t i, const float (&v)
   *reinterpret_cast<MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4)) = b;
 }
 
+// Non-temporal, at any element alignment: for results larger than the caches
+// or not read again soon, which then keep what is there.
+__device__ __forceinline__ void store8_once(bf16_t* p, int64_t i, const float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+  __builtin_nontemporal_store(w, reinterpret_cast<MUONH_GLOBAL u32x4_u*>(gmem(p + i)));
+}
+__device__ __forceinline__ void store8_once(float* p, int64_t i, const float (&v)[8]) {
+  const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+  __builtin_nontemporal_store(a, reinterpret_cast<MUONH_GLOBAL f32x4_u*>(gmem(p + i)));
+  __builtin_nontemporal_store(b, reinterpret_cast<MUONH_GLOBAL f32x4_u*>(gmem(p + i + 4)));
+}
+
 // Store one element of run-time dtype.
 __device__ __forceinline__ float store_dyn(void* p, int64_t i, float v, int dtype) {
   if (dtype == DT_BF16) {

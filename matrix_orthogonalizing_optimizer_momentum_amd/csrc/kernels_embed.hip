@@ -86,7 +86,9 @@ __global__ __launch_bounds__(kEmbThreads) void k_embedding(const EmbedArgs a, ui
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = key[k] < a.rows ? a.scale * v[e] : 0.f;
       const int64_t at = row[k] * a.width + col[k];
-      if (skip[k] == 0) {
+      if (skip[k] == 0 && a.once) {
+        store8_once(out, at, v);
+      } else if (skip[k] == 0) {
         store8_any(out, at, v);
       } else {
 #pragma unroll

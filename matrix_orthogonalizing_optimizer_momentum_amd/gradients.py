@@ -38,7 +38,7 @@ def _on(dev, stream):
     """Context in which allocations and launches go to ``stream`` on device
     ``dev``; gives the raw stream."""
     if stream is None and dev == torch.cuda.current_device():
-        return contextlib.nullcontext(torch.cuda.current_stream(dev).cuda_stream)
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(dev))
     return _switched(dev, stream)
 
 
@@ -49,25 +49,19 @@ def _check(rc, where):
 
 def _table(ts, what):
     """(pointers, sizes, dtype codes, device) of a list of gradients, checked."""
-    ptrs, sizes, codes = array("Q"), array("q"), array("i")
-    dev = -1
-    for t in ts:
-        code = _CODE.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{what}: unsupported dtype {t.dtype}: use torch.bfloat16 or torch.float32")
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError(f"{what}: tensors must be on the GPU")
-            if dev >= 0:
-                raise ValueError(f"{what}: tensors must be on one device")
-            dev = d
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: tensors must be contiguous")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-        codes.append(code)
-    return ptrs, sizes, codes, dev
+    codes = [_CODE.get(t.dtype, -1) for t in ts]
+    if -1 in codes:
+        raise TypeError(f"{what}: unsupported dtype {ts[codes.index(-1)].dtype}: use torch.bfloat16 or torch.float32")
+    devs = list(map(torch.Tensor.get_device, ts))
+    dev = devs[0]
+    if min(devs) < 0:
+        raise ValueError(f"{what}: tensors must be on the GPU")
+    if devs.count(dev) != len(devs):
+        raise ValueError(f"{what}: tensors must be on one device")
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError(f"{what}: tensors must be contiguous")
+    return (array("Q", map(torch.Tensor.data_ptr, ts)), array("q", map(torch.Tensor.numel, ts)), array("i", codes),
+            dev)
 
 
 def _addr(a):
@@ -91,13 +85,16 @@ def grad_norm(grads, max_norm=None, stream=None):
     lib = load()
     with _on(dev, stream) as raw:
         ws_bytes = lib.muonh_grad_norm_workspace(n)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=grads[0].device)
-        out = torch.empty(n + 2, dtype=torch.float32, device=grads[0].device)
-        p = out.data_ptr()
-        rc = lib.muonh_grad_norm(_addr(ptrs), _addr(sizes), _addr(codes), n, 0.0 if max_norm is None else max_norm,
-                                 p, None if max_norm is None else p + 4, p + 8, ws.data_ptr(), ws_bytes, raw)
+        where = grads[0].device
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=where)
+        norms = torch.empty(n, dtype=torch.float32, device=where)
+        total = torch.empty((), dtype=torch.float32, device=where)
+        coef = None if max_norm is None else torch.empty((), dtype=torch.float32, device=where)
+        rc = lib.muonh_grad_norm(_addr(ptrs), _addr(sizes), _addr(codes), n, 0.0 if coef is None else max_norm,
+                                 total.data_ptr(), None if coef is None else coef.data_ptr(), norms.data_ptr(),
+                                 ws.data_ptr(), ws_bytes, raw)
     _check(rc, "muonh_grad_norm")
-    return out[0], None if max_norm is None else out[1], out[2:]
+    return total, coef, norms
 
 
 def clip_grads(grads, max_norm, outputs=None, stream=None):
@@ -112,19 +109,22 @@ def clip_grads(grads, max_norm, outputs=None, stream=None):
     ptrs, sizes, codes, dev = _table(grads, "grads")
     outs = ptrs
     if outputs is not None:
+        if len(outputs) != n:
+            raise ValueError("outputs must have one tensor per gradient")
         outs, osizes, ocodes, odev = _table(outputs, "outputs")
         if osizes != sizes or ocodes != codes or odev != dev:
             raise ValueError("outputs must match grads in size, dtype and device")
     lib = load()
     with _on(dev, stream) as raw:
         ws_bytes = lib.muonh_grad_norm_workspace(n)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=grads[0].device)
-        out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
-        p = out.data_ptr()
-        rc = lib.muonh_clip_grads(_addr(ptrs), _addr(outs), _addr(sizes), _addr(codes), n, max_norm, p, p + 4,
-                                  ws.data_ptr(), ws_bytes, raw)
+        where = grads[0].device
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=where)
+        total = torch.empty((), dtype=torch.float32, device=where)
+        coef = torch.empty((), dtype=torch.float32, device=where)
+        rc = lib.muonh_clip_grads(_addr(ptrs), _addr(outs), _addr(sizes), _addr(codes), n, max_norm,
+                                  total.data_ptr(), coef.data_ptr(), ws.data_ptr(), ws_bytes, raw)
     _check(rc, "muonh_clip_grads")
-    return out[0], out[1]
+    return total, coef
 
 
 def _plain(t, what, dev=None):
