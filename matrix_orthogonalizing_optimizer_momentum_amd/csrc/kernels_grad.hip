@@ -13,7 +13,7 @@
 // (kTabTensors a launch), so a call uploads no table, keeps nothing between
 // calls and can be captured into a graph as it is.
 //
-// Work split: every tensor is cut into blocks of `chunk` elements, one for the
+// Work split: every tensor is cut into blocks of `chunk` bytes, one for the
 // whole call and chosen so that the blocks of all tensors together fill the
 // chip about once; a block sums its squares in fp64 (squares of bf16 and fp32
 // values neither overflow nor underflow there, and no order of the values
@@ -49,7 +49,7 @@ __device__ __forceinline__ int head_of(const void* p) {
 constexpr int kVec = 8;  // elements a thread takes at a time
 constexpr int kDepth = 4;  // such groups in flight
 
-template <typename T>
+template <bool ONCE, typename T>
 __device__ __forceinline__ double sumsq_block(const T* __restrict__ p, int64_t lo, int64_t hi) {
   const int t = threadIdx.x;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
@@ -73,7 +73,10 @@ __device__ __forceinline__ double sumsq_block(const T* __restrict__ p, int64_t l
   for (; i + (kDepth - 1) * kStep < v1; i += kDepth * kStep) {
     Raw8<T> r[kDepth];
 #pragma unroll
-    for (int k = 0; k < kDepth; ++k) r[k].load(p, i + k * kStep);
+    for (int k = 0; k < kDepth; ++k) {
+      if constexpr (ONCE) r[k].load_once(p, i + k * kStep);
+      else r[k].load(p, i + k * kStep);
+    }
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) add(r[k]);
   }
@@ -85,17 +88,20 @@ __device__ __forceinline__ double sumsq_block(const T* __restrict__ p, int64_t l
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+template <bool ONCE>
 __global__ __launch_bounds__(kGradThreads) void k_grad_sumsq(const GradTab tab, double* __restrict__ partials,
                                                              int32_t* __restrict__ bounds) {
   __shared__ double red[kGradThreads / 64];
   const int b = blockIdx.x;
   const int t = tensor_of(tab.first, tab.n, b);
   const int64_t n = tab.numel[t];
-  const int64_t lo = (int64_t)(b - tab.first[t]) * tab.chunk;
-  const int64_t hi = min(n, lo + tab.chunk);
+  const bool half = (tab.bf16[t >> 5] >> (t & 31)) & 1;
+  const int64_t per = tab.chunk >> (half ? 1 : 2);
+  const int64_t lo = (int64_t)(b - tab.first[t]) * per;
+  const int64_t hi = min(n, lo + per);
   double s;
-  if ((tab.bf16[t >> 5] >> (t & 31)) & 1) s = sumsq_block(reinterpret_cast<const bf16_t*>(tab.in[t]), lo, hi);
-  else s = sumsq_block(reinterpret_cast<const float*>(tab.in[t]), lo, hi);
+  if (half) s = sumsq_block<ONCE>(reinterpret_cast<const bf16_t*>(tab.in[t]), lo, hi);
+  else s = sumsq_block<ONCE>(reinterpret_cast<const float*>(tab.in[t]), lo, hi);
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -197,9 +203,11 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_scale(const ScaleTab tab,
   void* const out = tab.out[t];
   if (c == 1.f && in == out) return;  // nothing to change in place
   const int64_t n = tab.g.numel[t];
-  const int64_t lo = (int64_t)(b - tab.g.first[t]) * tab.g.chunk;
-  const int64_t hi = min(n, lo + tab.g.chunk);
-  if ((tab.g.bf16[t >> 5] >> (t & 31)) & 1)
+  const bool half = (tab.g.bf16[t >> 5] >> (t & 31)) & 1;
+  const int64_t per = tab.g.chunk >> (half ? 1 : 2);
+  const int64_t lo = (int64_t)(b - tab.g.first[t]) * per;
+  const int64_t hi = min(n, lo + per);
+  if (half)
     scale_block(reinterpret_cast<const bf16_t*>(in), reinterpret_cast<bf16_t*>(out), lo, hi, c);
   else
     scale_block(reinterpret_cast<const float*>(in), reinterpret_cast<float*>(out), lo, hi, c);
@@ -207,8 +215,10 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_scale(const ScaleTab tab,
 
 }  // namespace
 
-hipError_t launch_grad_sumsq(const GradTab& tab, int nblocks, double* partials, int32_t* bounds, hipStream_t s) {
-  hipLaunchKernelGGL(k_grad_sumsq, dim3(nblocks), dim3(kGradThreads), 0, s, tab, partials, bounds);
+hipError_t launch_grad_sumsq(const GradTab& tab, int nblocks, bool once, double* partials, int32_t* bounds,
+                             hipStream_t s) {
+  if (once) hipLaunchKernelGGL(k_grad_sumsq<true>, dim3(nblocks), dim3(kGradThreads), 0, s, tab, partials, bounds);
+  else hipLaunchKernelGGL(k_grad_sumsq<false>, dim3(nblocks), dim3(kGradThreads), 0, s, tab, partials, bounds);
   return hipGetLastError();
 }
 
