@@ -685,32 +685,30 @@ constexpr int kIndexThreads = 1024;
 __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) {
   __shared__ int32_t wsum[kIndexThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int PER = 8;
+  constexpr int PER = 8;  // 64-token rows of a wave, all its loads in flight together
   int64_t base = 0;
   for (int64_t i0 = 0; i0 < a.n; i0 += kIndexThreads * PER) {
-    int32_t t[PER];
-    int mine = 0;
+    const int64_t w0 = i0 + wave * (64 * PER) + lane;
+    int64_t t[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int64_t i = i0 + tid * PER + k;
-      int64_t v = -1;
-      if (i < a.n)
-        v = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[i]
-                            : gmem(reinterpret_cast<const int64_t*>(a.targets))[i];
-      const bool in = i < a.n && v >= 0 && v < a.rows && v != a.ignore_index;
-      t[k] = in ? (int32_t)v : -1;
-      mine += in;
-      if (i < a.n && !in && a.token_loss != nullptr) a.token_loss[i] = 0.f;
+      const int64_t i = min(w0 + 64 * k, a.n - 1);
+      t[k] = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[i]
+                             : gmem(reinterpret_cast<const int64_t*>(a.targets))[i];
     }
-    int incl = mine;
+    uint64_t in[PER];
+    int mine = 0;  // of the wave
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
+    for (int k = 0; k < PER; ++k) {
+      const int64_t i = w0 + 64 * k;
+      const bool ok = i < a.n && t[k] >= 0 && t[k] < a.rows && t[k] != a.ignore_index;
+      in[k] = __ballot(ok);
+      mine += __popcll(in[k]);
+      if (i < a.n && !ok && a.token_loss != nullptr) a.token_loss[i] = 0.f;
     }
-    if (lane == 63) wsum[wave] = incl;
+    if (lane == 0) wsum[wave] = mine;
     __syncthreads();
-    int64_t at = base + incl - mine;
+    int64_t at = base;
     int total = 0;
 #pragma unroll
     for (int w = 0; w < kIndexThreads / 64; ++w) {
@@ -718,12 +716,14 @@ __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) 
       total += wsum[w];
     }
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-      if (t[k] >= 0) {
-        a.perm[at] = (int32_t)(i0 + tid * PER + k);
-        a.tgt[at] = t[k];
-        ++at;
+    for (int k = 0; k < PER; ++k) {
+      if ((in[k] >> lane) & 1) {
+        const int64_t to = at + __popcll(in[k] & ((1ull << lane) - 1));
+        a.perm[to] = (int32_t)(w0 + 64 * k);
+        a.tgt[to] = (int32_t)t[k];
       }
+      at += __popcll(in[k]);
+    }
     base += total;
     __syncthreads();
   }
@@ -803,15 +803,24 @@ __global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
   if ((int64_t)blockIdx.x * 32 >= count) return;
   const int64_t tiles = a.rpad / kXTile;
   float m = -INFINITY, s = 0.f;
-  for (int64_t k = part; k < tiles; k += 8) {
-    const float2 q = a.stats[k * a.npad + ci];
-    const float nm = fmaxf(m, q.x);
-    if (nm != -INFINITY) {
-      s = s * __builtin_amdgcn_exp2f((m - nm) * kLog2e) + q.y * __builtin_amdgcn_exp2f((q.x - nm) * kLog2e);
-      m = nm;
-    } else {
-      s += q.y;  // 0, or a NaN to pass on
+  constexpr int U = 8;  // tiles in flight
+  for (int64_t k0 = part; k0 < tiles; k0 += 8 * U) {
+    float2 q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = a.stats[min(k0 + 8 * u, tiles - 1) * a.npad + ci];
+    float nm = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + 8 * u >= tiles) q[u] = make_float2(-INFINITY, 0.f);
+      nm = fmaxf(nm, q[u].x);
     }
+    // nothing finite so far: the sums are 0, or a NaN to pass on
+    const float b = nm == -INFINITY ? 0.f : nm;
+    s *= __builtin_amdgcn_exp2f((m - b) * kLog2e);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      s += q[u].x == -INFINITY ? q[u].y : q[u].y * __builtin_amdgcn_exp2f((q[u].x - b) * kLog2e);
+    m = nm;
   }
   sh[part][tl] = make_float2(m, s);
   __syncthreads();
