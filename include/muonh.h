@@ -417,7 +417,7 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
  * bf16 (at most 2^-8 of each value off), also where dw is fp32.
  * The vocabulary is taken in pieces for the gradients; the workspace decides
  * how large: muonh_cross_entropy_workspace gives the size for a `limit` in
- * bytes (0: pieces whose P takes up to 256 MiB; grads: 1 dx, 2 dw, 3 both; 0 is
+ * bytes (0: pieces whose P takes up to 512 MiB; grads: 1 dx, 2 dw, 3 both; 0 is
  * returned when the limit is below the smallest piece's need, or for invalid
  * sizes; only the address of w matters, its alignment).  A row of w that is
  * not a multiple of 64 values, or not on a 16-byte grid, is copied to the
