@@ -277,7 +277,8 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   // operand stages, then (STATS) the maximum and sum of each token per row of
   // waves.  One array: with the latter in an array of its own, which the
   // compiler placed first, the kernel ran 10% longer.
-  __shared__ __attribute__((aligned(16))) char smem[kXSmem + (STATS ? 4 * kXTile * (int)sizeof(float2) : 0)];
+  // For P the rest holds 4 KiB a wave (below).
+  __shared__ __attribute__((aligned(16))) char smem[kXSmem + (STATS ? 4 * kXTile * (int)sizeof(float2) : 8 * 4096)];
   float2* const st = reinterpret_cast<float2*>(smem + kXSmem);
   const int count = a.sc->count;
   const int ntok = (count + kXTile - 1) / kXTile;
@@ -447,7 +448,13 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] -= word(i, v) == t ? 1.f : 0.f;
         }
-        uint16_t* const row = a.prob + ci * p.cols + (vw - p.v0);
+        // Through LDS (chunks of 8 words, swizzled by token against bank
+        // conflicts), so that every store covers whole 128-byte lines, and past
+        // the caches, which P (up to 512 MiB) would only sweep: at 8192 tokens,
+        // 50257 words, width 768 this kernel takes 632 us, with stores of 32
+        // bytes a row 682; the products that read P 1183, 1267.  (The same for
+        // dw and dx's sums gained nothing.)
+        char* const own = smem + kXSmem + wv * 4096;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -460,8 +467,21 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
             const auto s0 = __builtin_amdgcn_permlane32_swap(w0, w2, false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(w1, w3, false, false);
             const u32x4_t pk = {s0[0], s1[0], s0[1], s1[1]};
-            *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(row + i * 32 + 16 * pq + 8 * hi)) = pk;
+            const int r = lane & 31, c = 4 * i + 2 * pq + hi;
+            *reinterpret_cast<u32x4_t*>(own + r * 128 + ((c ^ (r & 7)) * 16)) = pk;
           }
+        uint16_t* const block = a.prob + (tok0 + wn * WN + j * 32) * p.cols + (vw - p.v0);
+        u32x4_t line[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 8 * q + (lane >> 3), c = lane & 7;
+          line[q] = *reinterpret_cast<const u32x4_t*>(own + r * 128 + ((c ^ (r & 7)) * 16));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 8 * q + (lane >> 3), c = lane & 7;
+          __builtin_nontemporal_store(line[q], reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(block + r * p.cols + c * 8)));
+        }
       }
     }
   };
