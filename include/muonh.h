@@ -341,7 +341,7 @@ int frob_project(void* const W[], const void* const U[], const int64_t shapes[],
  * clipped gradients with no further pass over them.
  *   grads[t]   device, numel[t] elements of dtypes[t] (MUONH_F32 / MUONH_BF16),
  *              contiguous, aligned to the element; may be NULL if numel[t] = 0
- *   numel      host, n int64, >= 0;  dtypes  host, n ints;  n >= 1
+ *   numel      host, n int64, >= 0;  dtypes  host, n ints;  n  1 .. 2^24
  *   max_norm   finite, >= 0; ignored when coef is NULL
  *   total      device, 1 float
  *   coef       device, 1 float, or NULL
@@ -369,8 +369,8 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
  *   table   device, rows x width, MUONH_F32 (master weights) or MUONH_BF16
  *   ids     device, n integers of id_bits (32 or 64), signed
  *   out     device, n x width, MUONH_F32 or MUONH_BF16 (one rounding)
- *   n       0 .. 2^31 - 1;  rows  1 .. 2^31 - 2;  width  1 .. 2^18 (larger:
- *           MUONH_ENOTIMPL);  scale  finite
+ *   rows    1 .. 2^31 - 2;  n  0 .. 2^26, width  1 .. 2^18, together up to 2^36
+ *           values of out (more: MUONH_ENOTIMPL);  scale  finite
  * Buffers need no more than their elements' alignment.
  */
 int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t width, const void* ids, int id_bits,
@@ -407,8 +407,8 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
  * counted the loss and both gradients are zero.
  *   x           device, n x width, bf16;  w  device, rows x width, bf16
  *   targets     device, n integers of id_bits (32 or 64), signed
- *   n           0 .. 2^30; rows 1 .. 2^31 - 2; width 1 .. 65536 (MUONH_ENOTIMPL
- *               above that, and above 2^31 tiles of 256 tokens x 256 rows)
+ *   n           0 .. 2^22; rows 1 .. 2^23; width 1 .. 65536; up to 2^34 values
+ *               of x (MUONH_ENOTIMPL above)
  *   loss        device, 1 float;  token_loss  device, n floats, or NULL
  *   dx          device, n x width, bf16, or NULL (not computed)
  *   dw          device, rows x width of dw_dtype (MUONH_BF16 / MUONH_F32), or

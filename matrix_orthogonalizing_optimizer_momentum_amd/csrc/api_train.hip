@@ -41,6 +41,7 @@ int64_t grad_chunk(int64_t bytes) {
 // total: bytes of all gradients.
 int check_grads(const void* const* grads, const int64_t* numel, const int* dtypes, int n, int64_t& total) {
   if (!grads || !numel || !dtypes || n <= 0) return MUONH_EINVAL;
+  if (n > (1 << 24)) return MUONH_ENOTIMPL;
   total = 0;
   for (int i = 0; i < n; ++i) {
     if (numel[i] < 0 || numel[i] > ((int64_t)1 << 46)) return MUONH_EINVAL;
@@ -96,10 +97,12 @@ bool misaligned(const void* p, int64_t a) { return (uintptr_t)p % a != 0; }
 
 // n tokens, a table of rows x width; n = 0 is allowed.
 int check_embedding(const void* ids, int id_bits, int64_t n, int64_t rows, int64_t width) {
-  if (n < 0 || n > INT32_MAX || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;
+  if (n < 0 || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;
   if (id_bits != 32 && id_bits != 64) return MUONH_EINVAL;
   if (n > 0 && (!ids || misaligned(ids, id_bits / 8))) return MUONH_EINVAL;
-  return width > kEmbMaxWidth ? MUONH_ENOTIMPL : MUONH_OK;
+  // what the kernels' grids hold (below 2^32 threads a launch)
+  return width > kEmbMaxWidth || n > kEmbMaxTokens || n * up(width, 8) > ((int64_t)1 << 36) ? MUONH_ENOTIMPL
+                                                                                              : MUONH_OK;
 }
 
 // Scratch of the embedding gradient.
@@ -155,12 +158,10 @@ struct XentPlan {
 constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
 
 int check_xent(const void* w, int64_t n, int64_t rows, int64_t width) {
-  if (n < 0 || n > ((int64_t)1 << 30) || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;
-  if (width > kXMaxWidth) return MUONH_ENOTIMPL;
-  if (w && misaligned(w, 2)) return MUONH_EINVAL;
-  // tiles of one launch
-  if (up(n, kXTile) / kXTile * (up(rows, kXTile) / kXTile) > INT32_MAX) return MUONH_ENOTIMPL;
-  return MUONH_OK;
+  if (n < 0 || rows < 1 || width < 1 || (w && misaligned(w, 2))) return MUONH_EINVAL;
+  // what the kernels' grids hold (below 2^32 threads a launch)
+  if (n > kXMaxTokens || rows > kXMaxRows || width > kXMaxWidth) return MUONH_ENOTIMPL;
+  return up(n, kXTile) * up(width, kXTile) > ((int64_t)1 << 34) ? MUONH_ENOTIMPL : MUONH_OK;
 }
 
 // Time of a launch in units of one operand stage: n1 jobs of c1, then n2 of c2,
@@ -338,7 +339,8 @@ int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t wi
 }
 
 size_t muonh_embedding_grad_workspace(int64_t n, int64_t rows, int64_t width) {
-  if (check_embedding(nullptr, 32, 0, rows, width) != MUONH_OK || n < 0 || n > INT32_MAX) return 0;
+  alignas(4) static const char any[4] = {};  // a pointer that passes for the ids
+  if (check_embedding(any, 32, n, rows, width) != MUONH_OK) return 0;
   return (size_t)embed_plan(n, rows, width).bytes;
 }
 

@@ -10,7 +10,7 @@ namespace muonh {
 // caches, which leaves them to the table's frequent rows: 65536 x 2048 bf16
 // (268 MB) 90 -> 82 us.
 constexpr int64_t kEmbOnceBytes = (int64_t)128 << 20;
-constexpr int64_t kEmbMaxWidth = (int64_t)1 << 18;
+constexpr int64_t kEmbMaxWidth = (int64_t)1 << 18, kEmbMaxTokens = (int64_t)1 << 26;
 constexpr int kSortThreads = 256;
 constexpr int kSortBits = 11;      // digit bits of one sort pass, at most
 constexpr int kSortMaxBlocks = 64;

@@ -625,7 +625,6 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
         [=](int s) { return pt + (int64_t)s * kXStage * ldp; }, ldp, ldp - vl, acc);
     const float g = a.sc->gscale;
     WT* const dw = reinterpret_cast<WT*>(a.dw);
-    const bool vec = a.width % 8 == 0 && (uintptr_t)dw % 16 == 0;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t v = p.v0 + vl + wn * WN + j * 32 + (lane & 31);
@@ -644,14 +643,14 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
           const int64_t d = d0 + wm * WM + i * 32 + 16 * pq + 8 * hi;
           if (v >= a.rows || d >= a.width) continue;
           const int64_t at = v * a.width + d;
-          if (vec) {
+          if (d + 8 <= a.width) {
             if (a.accumulate) {
               float old[8];
-              load8(dw, at, old);
+              load8_any(dw, at, old);
 #pragma unroll
               for (int k = 0; k < 8; ++k) e[k] += old[k];
             }
-            store8(dw, at, e);
+            store8_any(dw, at, e);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -757,12 +756,12 @@ __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) 
 
 // Rows of `width` values copied to rows of `ld`, zero padded: element e of an
 // 8-element chunk past the row or its end is 0.
-__device__ __forceinline__ void copy_chunk(const uint16_t* src, bool row_ok, int64_t width, bool vec, int64_t col,
+__device__ __forceinline__ void copy_chunk(const uint16_t* src, bool row_ok, int64_t width, int64_t col,
                                            uint16_t* dst) {
   u32x4_t q = {0u, 0u, 0u, 0u};
   if (row_ok) {
-    if (vec && col + 8 <= width) {
-      q = *reinterpret_cast<const MUONH_GLOBAL u32x4_t*>(gmem(src + col));
+    if (col + 8 <= width) {
+      q = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(src + col));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -782,14 +781,12 @@ __global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uin
   if (b < a.npad) {
     const bool ok = b < a.sc->count;
     const uint16_t* const src = a.x + (ok ? (int64_t)a.perm[b] : 0) * a.width;
-    const bool vec = a.width % 8 == 0 && (uintptr_t)a.x % 16 == 0;
-    for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8) copy_chunk(src, ok, a.width, vec, c, a.xp + b * a.wpad);
+    for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8) copy_chunk(src, ok, a.width, c, a.xp + b * a.wpad);
     return;
   }
   const int64_t r = b - a.npad, v = w0 + r;
-  const bool vec = a.width % 8 == 0 && (uintptr_t)w_in % 16 == 0;
   for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8)
-    copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, vec, c, w_out + r * a.wpad);
+    copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, c, w_out + r * a.wpad);
 }
 
 // xt = xp transposed, 64 x 64 values a block.
@@ -883,7 +880,6 @@ __global__ __launch_bounds__(1024) void k_xent_total(const XentArgs a) {
 // written by the blocks after them, one a token.
 __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
   const int64_t b = blockIdx.x;
-  const bool vec = a.width % 8 == 0 && (uintptr_t)a.dx % 16 == 0;
   const int count = a.sc->count;
   int64_t token;
   bool zero = false;
@@ -911,7 +907,7 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
       for (int x = 0; x < 8; ++x) e[x] *= g;
     }
     const int64_t at = token * a.width + c;
-    if (vec) store8(a.dx, at, e);
+    if (c + 8 <= a.width) store8_any(a.dx, at, e);
     else
       for (int x = 0; x < 8; ++x)
         if (c + x < a.width) St<bf16_t>::st(a.dx, at + x, e[x]);

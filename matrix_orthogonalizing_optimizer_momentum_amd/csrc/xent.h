@@ -10,7 +10,7 @@ constexpr int kXTile = 256;          // output tile side of the products
 constexpr int kXStage = 64;          // depth of one operand stage
 constexpr int kXCus = 256;            // compute units, a multiple of the 8 XCDs
 constexpr int kXMaxSplits = 8;
-constexpr int64_t kXMaxWidth = 65536;
+constexpr int64_t kXMaxWidth = 65536, kXMaxTokens = (int64_t)1 << 22, kXMaxRows = (int64_t)1 << 23;
 
 // Device scalars of one call.
 struct XentScalars {
