@@ -135,10 +135,10 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
     p.pos[k] = take(4 * n);
   }
   p.hist = take(4 * ((int64_t)p.blocks << p.bits));
-  // Pieces as long as leave 16 waves a CU (a wave takes 512 columns of a piece):
+  // Pieces as long as leave 8 waves a CU (a wave takes 512 columns of a piece):
   // long ones save partial rows, short ones fill the chip at few tokens.
   p.run = kRunMax;
-  while (p.run > kRunMin && (n + p.run - 1) / p.run * ((width + 511) / 512) < 4096) p.run /= 2;
+  while (p.run > kRunMin && (n + p.run - 1) / p.run * ((width + 511) / 512) < 2048) p.run /= 2;
   p.part = take(8 * ((n + p.run - 1) / p.run) * up(width, 8));
   p.bytes = std::max<int64_t>(at, 256);
   return p;

@@ -18,7 +18,7 @@ constexpr int kSoloThreads = 1024;  // the sort in one workgroup:
 constexpr int kSoloItems = 8;       // tokens per thread (8192 tokens on 50257 x 768: 37 us, by passes 52; 16384: 61 and 56)
 constexpr int kSoloBits = 9;        // digit bits of one of its passes
 constexpr int64_t kSoloTokens = kSoloThreads * kSoloItems;
-constexpr int kRunMin = 8, kRunMax = 32;  // sorted tokens per piece of the gradient
+constexpr int kRunMin = 8, kRunMax = 64;  // sorted tokens per piece of the gradient
 
 // A share of the table's gradient that a launch clears: slice `index` of
 // `count` equal ones (count 0: nothing).  p is aligned to 2 bytes.

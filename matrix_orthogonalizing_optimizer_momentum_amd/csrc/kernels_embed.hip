@@ -187,7 +187,15 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p,
   const int64_t wlo = min(p.n, lo + (int64_t)wave * quarter), whi = min(p.n, wlo + quarter);
   for (uint32_t d = tid; d < kSortWaves * bins; d += kSortThreads) next[d / bins][d % bins] = 0;
   __syncthreads();
-  for (int64_t i = wlo + lane; i < whi; i += 64) atomicAdd(&next[wave][(pass_key(p, i) >> p.shift) & (bins - 1)], 1u);
+  constexpr int R = 4;  // rows of 64 tokens in flight
+  for (int64_t i0 = wlo + lane; i0 < whi; i0 += 64 * R) {
+    uint32_t k[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) k[r] = pass_key(p, min(i0 + 64 * r, whi - 1));
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i0 + 64 * r < whi) atomicAdd(&next[wave][(k[r] >> p.shift) & (bins - 1)], 1u);
+  }
   __syncthreads();
   // Thread t owns the digits [t * per, (t + 1) * per): the place of a digit's
   // first token in this block is the number of tokens with smaller digits
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p,
     if (k < per && owner) {
       const uint32_t d = tid * per + k;
       // a batch of blocks' counts in flight at a time
-      constexpr int B = 16;
+      constexpr int B = kSortMaxBlocks / 2;
       for (int b0 = 0; b0 < p.blocks; b0 += B) {
         uint32_t c[B];
 #pragma unroll
@@ -243,15 +251,22 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p,
   }
   __syncthreads();
   // 64 tokens at a time, in order
-  for (int64_t i0 = wlo; i0 < whi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const bool in = i < whi;
-    const uint32_t key = in ? pass_key(p, i) : 0u;
-    const uint32_t pos = in ? (p.ids != nullptr ? (uint32_t)i : gmem(p.pos_in)[i]) : 0u;
-    const uint32_t at = take_place(next[wave], (key >> p.shift) & (bins - 1), p.bits, in);
-    if (in) {
-      gmem(p.key_out)[at] = key;
-      gmem(p.pos_out)[at] = pos;
+  for (int64_t i0 = wlo; i0 < whi; i0 += 64 * R) {
+    uint32_t key[R], pos[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = min(i0 + 64 * r + lane, whi - 1);
+      key[r] = pass_key(p, i);
+      pos[r] = p.ids != nullptr ? (uint32_t)i : gmem(p.pos_in)[i];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = i0 + 64 * r + lane < whi;
+      const uint32_t at = take_place(next[wave], (key[r] >> p.shift) & (bins - 1), p.bits, in);
+      if (in) {
+        gmem(p.key_out)[at] = key[r];
+        gmem(p.pos_out)[at] = pos[r];
+      }
     }
   }
 }
