@@ -210,7 +210,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(const SortPass p,
     if (k < per && owner) {
       const uint32_t d = tid * per + k;
       // a batch of blocks' counts in flight at a time
-      constexpr int B = kSortMaxBlocks / 2;
+      constexpr int B = 32;
       for (int b0 = 0; b0 < p.blocks; b0 += B) {
         uint32_t c[B];
 #pragma unroll
