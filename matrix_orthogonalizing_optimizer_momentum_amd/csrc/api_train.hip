@@ -257,6 +257,7 @@ int xent_plan(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bo
     const int64_t step = std::max<int64_t>(1, top / 32);
     for (int64_t tiles = top; tiles > top / 2; tiles -= step)
       for (int64_t splits = 1; splits <= kXMaxSplits && splits <= tiles; splits *= 2) {
+        if (splits > 1 && 4 * splits * npad * wpad > kXSplitBytes) break;
         if (xent_layout(w, n, rows, width, dx, dw, tiles * kXTile, splits).bytes > limit) continue;
         const int64_t t = xent_cost(ntok, nvoc, wpad, tiles, splits);
         if (best_tiles == 0 || t < best) {

@@ -9,7 +9,11 @@ namespace muonh {
 constexpr int kXTile = 256;          // output tile side of the products
 constexpr int kXStage = 64;          // depth of one operand stage
 constexpr int kXCus = 256;            // compute units, a multiple of the 8 XCDs
-constexpr int kXMaxSplits = 8;
+// Parts that dx is summed in: many at few tokens, where dx has few tiles and
+// each is as deep as a piece (256 tokens, 50257 words, width 768: 224 us with up
+// to 8 parts, 151 with up to 64), within a bound on their size.
+constexpr int kXMaxSplits = 64;
+constexpr int64_t kXSplitBytes = (int64_t)256 << 20;
 constexpr int64_t kXMaxWidth = 65536, kXMaxTokens = (int64_t)1 << 22, kXMaxRows = (int64_t)1 << 23;
 
 // Device scalars of one call.
