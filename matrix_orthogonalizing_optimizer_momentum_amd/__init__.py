@@ -476,4 +476,9 @@ def profile_read():
     return out
 
 
-from .gradients import clip_grads, cross_entropy, embedding, embedding_grad, grad_norm  # noqa: E402,F401
+def __getattr__(name):
+    # gradients.py needs torch at import, which nothing above does
+    if name in ("clip_grads", "cross_entropy", "embedding", "embedding_grad", "grad_norm"):
+        from . import gradients
+        return getattr(gradients, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -3,7 +3,9 @@
     python -m matrix_orthogonalizing_optimizer_momentum_amd.build
 
 compiles every csrc/*.hip with hipcc --offload-arch=gfx950, the host-only
-planner with g++, and links them into libmuonh.so next to this file.
+planner with g++, and links them into libmuonh.so next to this file; beside it
+_tensors.so, the Python extension that reads lists of torch tensors
+(binding/tensors.cpp, host code only).
 """
 from __future__ import annotations
 
@@ -12,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libmuonh.so")
+BINDING = os.path.join(HERE, "binding", "tensors.cpp")
+BINDING_OUT = os.path.join(HERE, "_tensors.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "muonh")
 
 ARCH = os.environ.get("MUONH_ARCH", "gfx950")
@@ -49,6 +54,17 @@ def sources():
     return hip, cpp
 
 
+def binding_cmd(out):
+    """The g++ line of the tensor-list extension, against the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    return ["g++", *HOST_FLAGS, "-shared", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
+            f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING, "-o", out,
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compile and link; returns the path of the built library."""
     if not os.path.exists(HIPCC):
@@ -65,6 +81,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
         cmds.append(["g++", *HOST_FLAGS, "-c", src, "-o", obj])
         objs.append(obj)
+    cmds.append(binding_cmd(BINDING_OUT + ".tmp"))
     jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 4)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         for out in ex.map(_run, cmds):
@@ -73,13 +90,15 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     tmp = OUT + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, OUT)
+    os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
     return OUT
 
 
 def clean():
     shutil.rmtree(BUILD_DIR, ignore_errors=True)
-    if os.path.exists(OUT):
-        os.remove(OUT)
+    for f in (OUT, BINDING_OUT):
+        if os.path.exists(f):
+            os.remove(f)
 
 
 if __name__ == "__main__":

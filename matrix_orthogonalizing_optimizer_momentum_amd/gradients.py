@@ -10,14 +10,16 @@ call can be captured into a graph.
 from __future__ import annotations
 
 import contextlib
-import ctypes
-from array import array
-from ctypes import c_void_p
 
 import torch
 
 from . import (MUONH_BF16, MUONH_ENOMEM, MUONH_F32, MUONH_REDUCE_MEAN, MUONH_REDUCE_SUM, MuonhError,
-               load)
+               MuonhUnavailable, load)
+
+try:
+    from . import _tensors
+except ImportError:  # not built
+    _tensors = None
 
 _CODE = {torch.float32: MUONH_F32, torch.bfloat16: MUONH_BF16}
 
@@ -49,23 +51,9 @@ def _check(rc, where):
 
 def _table(ts, what):
     """(pointers, sizes, dtype codes, device) of a list of gradients, checked."""
-    codes = [_CODE.get(t.dtype, -1) for t in ts]
-    if -1 in codes:
-        raise TypeError(f"{what}: unsupported dtype {ts[codes.index(-1)].dtype}: use torch.bfloat16 or torch.float32")
-    devs = list(map(torch.Tensor.get_device, ts))
-    dev = devs[0]
-    if min(devs) < 0:
-        raise ValueError(f"{what}: tensors must be on the GPU")
-    if devs.count(dev) != len(devs):
-        raise ValueError(f"{what}: tensors must be on one device")
-    if not all(map(torch.Tensor.is_contiguous, ts)):
-        raise ValueError(f"{what}: tensors must be contiguous")
-    return (array("Q", map(torch.Tensor.data_ptr, ts)), array("q", map(torch.Tensor.numel, ts)), array("i", codes),
-            dev)
-
-
-def _addr(a):
-    return a.buffer_info()[0]
+    if _tensors is None:
+        raise MuonhUnavailable("_tensors.so is not built; run `python -m matrix_orthogonalizing_optimizer_momentum_amd.build`")
+    return _tensors.table(ts, what)
 
 
 def grad_norm(grads, max_norm=None, stream=None):
@@ -90,7 +78,7 @@ def grad_norm(grads, max_norm=None, stream=None):
         norms = torch.empty(n, dtype=torch.float32, device=where)
         total = torch.empty((), dtype=torch.float32, device=where)
         coef = None if max_norm is None else torch.empty((), dtype=torch.float32, device=where)
-        rc = lib.muonh_grad_norm(_addr(ptrs), _addr(sizes), _addr(codes), n, 0.0 if coef is None else max_norm,
+        rc = lib.muonh_grad_norm(ptrs, sizes, codes, n, 0.0 if coef is None else max_norm,
                                  total.data_ptr(), None if coef is None else coef.data_ptr(), norms.data_ptr(),
                                  ws.data_ptr(), ws_bytes, raw)
     _check(rc, "muonh_grad_norm")
@@ -121,7 +109,7 @@ def clip_grads(grads, max_norm, outputs=None, stream=None):
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=where)
         total = torch.empty((), dtype=torch.float32, device=where)
         coef = torch.empty((), dtype=torch.float32, device=where)
-        rc = lib.muonh_clip_grads(_addr(ptrs), _addr(outs), _addr(sizes), _addr(codes), n, max_norm,
+        rc = lib.muonh_clip_grads(ptrs, outs, sizes, codes, n, max_norm,
                                   total.data_ptr(), coef.data_ptr(), ws.data_ptr(), ws_bytes, raw)
     _check(rc, "muonh_clip_grads")
     return total, coef

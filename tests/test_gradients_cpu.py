@@ -165,6 +165,16 @@ def test_python_checks():
         mm.make_opts(grad_scale=torch.ones(1), stream=0)
 
 
+def test_tensor_lists():
+    from matrix_orthogonalizing_optimizer_momentum_amd import _tensors
+    assert _tensors.table([], "x") == (b"", b"", b"", -1)
+    a = torch.zeros(4)
+    for bad, err in ((3, TypeError), ([a, 3], ValueError), ([3], TypeError), ([None], TypeError), ([a], ValueError),
+                     ([a.half()], TypeError), ([a.to_sparse()], ValueError)):
+        with pytest.raises(err):
+            _tensors.table(bad, "x")
+
+
 def test_options_carry_the_scale():
     o = mm.Opts()
     mm.load().muonh_default_opts(ctypes.byref(o))
