@@ -356,8 +356,9 @@ int muonh_grad_norm(const void* const grads[], const int64_t numel[], const int 
 /*
  * muonh_clip_grads -- muonh_grad_norm, then outs[t] = coef * grads[t] in the
  * gradient's own dtype (one rounding).  outs[t] may be grads[t] (in place;
- * nothing is written when coef is 1), else the buffers must not overlap.
- * Workspace: muonh_grad_norm_workspace(n).
+ * nothing is written when coef is 1), else the buffers must not overlap; a
+ * buffer listed twice among outs is refused.  Workspace:
+ * muonh_grad_norm_workspace(n).
  */
 int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_t numel[], const int dtypes[], int n,
                      float max_norm, float* total, float* coef, void* workspace, size_t workspace_bytes,
@@ -413,6 +414,7 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
  *   dx          device, n x width, bf16, or NULL (not computed)
  *   dw          device, rows x width of dw_dtype (MUONH_BF16 / MUONH_F32), or
  *               NULL; accumulate = 1 adds to it (gradient accumulation)
+ * No output may overlap w, targets or another output (dx may be x).
  * Products take bf16 operands and sum in fp32.  The gradients see P rounded to
  * bf16 (at most 2^-8 of each value off), also where dw is fp32.
  * The vocabulary is taken in pieces for the gradients; the workspace decides

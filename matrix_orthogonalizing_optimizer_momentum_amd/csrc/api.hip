@@ -6,7 +6,6 @@
 //   k_hook_reduce, k_hook_write          (Hyperball or RadialBrake)
 // all queued on the caller's stream with no host synchronization.
 #include <hip/hip_runtime.h>
-#include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -62,13 +61,6 @@ static thread_local char g_last_error[256] = "";
 int hip_fail(hipError_t e, const char* what) {
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
   return MUONH_EHIP;
-}
-
-void set_error(const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-  va_end(ap);
 }
 
 namespace {

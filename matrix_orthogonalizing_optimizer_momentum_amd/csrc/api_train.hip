@@ -6,6 +6,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "desc.h"
 #include "embed.h"
@@ -51,6 +53,17 @@ int check_grads(const void* const* grads, const int64_t* numel, const int* dtype
     total += grad_bytes(numel[i], dtypes[i]);
   }
   return total > ((int64_t)1 << 50) ? MUONH_EINVAL : MUONH_OK;
+}
+
+// Whether a buffer is listed twice (writes to it would race).
+int check_distinct(void* const* outs, const int64_t* numel, int n) {
+  std::unique_ptr<uintptr_t[]> v(new (std::nothrow) uintptr_t[n]);
+  if (!v) return MUONH_ENOMEM;
+  int m = 0;
+  for (int i = 0; i < n; ++i)
+    if (numel[i] > 0) v[m++] = (uintptr_t)outs[i];
+  std::sort(v.get(), v.get() + m);
+  return std::adjacent_find(v.get(), v.get() + m) == v.get() + m ? MUONH_OK : MUONH_EINVAL;
 }
 
 // The table of tensors [i0, i0 + t.n) and its number of blocks.
@@ -148,7 +161,7 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
 // Scratch of one call: what every call needs, then what the gradients need.
 struct XentPlan {
   bool copy_w;
-  int64_t npad, rpad, wpad, wfull, ldxt, cols, splits, pieces;
+  int64_t npad, rpad, wpad, wfull, ldxt, cols, splits;
   int64_t sc, xp, xt, perm, tgt, lse, tlogit, wcopy, area, dxacc, bytes;
 };
 
@@ -233,7 +246,6 @@ XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool
   // the statistics are read before the first piece's P is written
   p.area = take(std::max<int64_t>(8 * (p.rpad / kXTile) * p.npad, 2 * p.npad * cols));
   if (cols > 0) {
-    p.pieces = (p.rpad + cols - 1) / cols;
     p.splits = splits;
     if (dx) p.dxacc = take(4 * p.splits * p.npad * p.wpad);
   }
@@ -308,6 +320,8 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
   for (int i = 0; i < n; ++i)
     if (numel[i] > 0 && (!outs[i] || (uintptr_t)outs[i] % (dtypes[i] == MUONH_F32 ? 4 : 2) != 0)) return MUONH_EINVAL;
   if (!std::isfinite(max_norm) || max_norm < 0.f) return MUONH_EINVAL;
+  const int rd = check_distinct(outs, numel, n);
+  if (rd != MUONH_OK) return rd;
   if (workspace_bytes < muonh_grad_norm_workspace(n)) return MUONH_ENOMEM;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int rq = queue_norm(grads, numel, dtypes, n, bytes, false, max_norm, total, coef, nullptr, workspace, s);

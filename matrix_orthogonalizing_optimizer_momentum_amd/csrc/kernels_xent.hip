@@ -21,8 +21,9 @@
 // double buffered in LDS, brought in by direct global -> LDS loads; the two
 // waves of a SIMD alternate between reading fragments and running MFMAs.  An
 // operand whose rows run along k is read as it is; one stored [k][m] is read
-// through gfx950's transposing LDS read, so neither P, x nor w is ever
-// transposed in memory.  The side a lane holds four consecutive values of (m)
+// through gfx950's transposing LDS read, so that neither P nor w is transposed
+// in memory (x is, once: dw needs both its operands along the tokens, and
+// transposing reads of both would bound it by LDS).  The side a lane holds four consecutive values of (m)
 // is the one the result's rows run along: words for P, width for dx and dw.
 #include <type_traits>
 
@@ -43,7 +44,6 @@ constexpr int kOperand = kXTile * kXStage;        // elements of one operand sta
 constexpr int kOperandB = kOperand * 2;           // 32 KiB
 constexpr int kXSmem = 4 * kOperandB;             // two stages of two operands
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0)
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }     // lgkmcnt(0)
@@ -749,7 +749,6 @@ __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) 
   if (tid == 0) {
     const double c = a.mean ? 1.0 / (double)max<int64_t>(base, 1) : 1.0;
     a.sc->count = (int32_t)base;
-    a.sc->scale = (float)c;
     a.sc->gscale = (float)(c * (double)a.grad_scale);
   }
 }

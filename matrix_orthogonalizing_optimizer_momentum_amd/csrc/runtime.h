@@ -14,8 +14,6 @@ enum {
 
 // Records e as this thread's last HIP failure and returns MUONH_EHIP.
 int hip_fail(hipError_t e, const char* what);
-// Sets this thread's muonh_last_error() text (printf style).
-void set_error(const char* fmt, ...);
 
 #define MUONH_TRY_HIP(x)                                  \
   do {                                                    \

@@ -19,7 +19,6 @@ constexpr int64_t kXMaxWidth = 65536, kXMaxTokens = (int64_t)1 << 22, kXMaxRows 
 // Device scalars of one call.
 struct XentScalars {
   int32_t count;                     // counted tokens
-  float scale;                       // factor of the loss (1 or 1 / count)
   float gscale;                      // factor of both gradients
 };
 

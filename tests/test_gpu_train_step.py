@@ -266,6 +266,27 @@ def test_embedding_off_the_grid(width, k):
         assert bool((rows[:k] == 7).all()) and bool((rows[k + 700 * width:] == 7).all())
 
 
+def test_gradient_of_x_in_its_place():
+    print("[case] dx over x", flush=True)
+    x = torch.randn(300, 128, device=DEV).bfloat16()
+    w = (torch.randn(500, 128, device=DEV) * 0.2).bfloat16()
+    t = torch.randint(0, 500, (300,), device=DEV)
+    want = mm.cross_entropy(x, w, t)
+    got = mm.cross_entropy(x, w, t, dx=x)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert got[2].data_ptr() == x.data_ptr()
+
+
+def test_a_gradient_listed_twice():
+    print("[case] listed twice", flush=True)
+    g = torch.randn(1000, device=DEV)
+    total, _, norms = mm.grad_norm([g, g])
+    assert abs(float(total) - math.sqrt(2) * float(norms[0])) <= 2.0 ** -22 * float(total)
+    with pytest.raises(mm.MuonhError):
+        mm.clip_grads([g, g], 1.0)
+
+
 def test_python_refusals():
     print("[case] refusals", flush=True)
     t, i = torch.randn(6, 8, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)

@@ -39,7 +39,7 @@ def test_norm_and_clip_refuse(clip, kw):
     assert norm(clip, **kw) == mm.MUONH_EINVAL
 
 
-@pytest.mark.parametrize("kw", [dict(null="o"), dict(outs=(0, P)), dict(outs=(P, P + 1)), dict(coef=None)])
+@pytest.mark.parametrize("kw", [dict(null="o"), dict(outs=(0, P)), dict(outs=(P, P + 1)), dict(coef=None), dict(outs=(P, P))])
 def test_clip_refuses(kw):
     assert norm(True, **kw) == mm.MUONH_EINVAL
 
