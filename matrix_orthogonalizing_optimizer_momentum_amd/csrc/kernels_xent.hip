@@ -699,6 +699,19 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 // ---------------------------------------------------------------------------
 // around the products
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ int64_t target_of(const XentArgs& a, int64_t i) {
+  return a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[i]
+                         : gmem(reinterpret_cast<const int64_t*>(a.targets))[i];
+}
+__device__ __forceinline__ bool counted(const XentArgs& a, int64_t t) {
+  return t >= 0 && t < a.rows && t != a.ignore_index;
+}
+__device__ __forceinline__ void put_scalars(const XentArgs& a, int64_t count) {
+  const double c = a.mean ? 1.0 / (double)max<int64_t>(count, 1) : 1.0;
+  a.sc->count = (int32_t)count;
+  a.sc->gscale = (float)(c * (double)a.grad_scale);
+}
+
 // One workgroup: the list of counted tokens in batch order, and the factors.
 constexpr int kIndexThreads = 1024;
 __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) {
@@ -712,15 +725,14 @@ __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) 
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int64_t i = min(w0 + 64 * k, a.n - 1);
-      t[k] = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[i]
-                             : gmem(reinterpret_cast<const int64_t*>(a.targets))[i];
+      t[k] = target_of(a, i);
     }
     uint64_t in[PER];
     int mine = 0;  // of the wave
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int64_t i = w0 + 64 * k;
-      const bool ok = i < a.n && t[k] >= 0 && t[k] < a.rows && t[k] != a.ignore_index;
+      const bool ok = i < a.n && counted(a, t[k]);
       in[k] = __ballot(ok);
       mine += __popcll(in[k]);
       if (i < a.n && !ok && a.token_loss != nullptr) a.token_loss[i] = 0.f;
@@ -746,11 +758,7 @@ __global__ __launch_bounds__(kIndexThreads) void k_xent_index(const XentArgs a) 
     base += total;
     __syncthreads();
   }
-  if (tid == 0) {
-    const double c = a.mean ? 1.0 / (double)max<int64_t>(base, 1) : 1.0;
-    a.sc->count = (int32_t)base;
-    a.sc->gscale = (float)(c * (double)a.grad_scale);
-  }
+  if (tid == 0) put_scalars(a, base);
 }
 
 // Rows of `width` values copied to rows of `ld`, zero padded: element e of an
@@ -773,13 +781,63 @@ __device__ __forceinline__ void copy_chunk(const uint16_t* src, bool row_ok, int
 }
 
 // Blocks [0, npad): one row of xp each (counted tokens of x, then zeros); the
-// others: one row of the padded copy of the weights from row w0 on.
+// others: one row of the padded copy of the weights from row w0 on.  LIST: up
+// to kXListTokens tokens, where every block finds its token itself and the
+// first one writes the list, which saves k_xent_index.
+template <bool LIST>
 __global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uint16_t* w_in, uint16_t* w_out,
                                                      int64_t w0) {
   const int64_t b = blockIdx.x;
   if (b < a.npad) {
-    const bool ok = b < a.sc->count;
-    const uint16_t* const src = a.x + (ok ? (int64_t)a.perm[b] : 0) * a.width;
+    bool ok;
+    int64_t token;
+    if constexpr (LIST) {
+      constexpr int PER = (int)(kXListTokens / 256);
+      __shared__ int32_t part[4];
+      __shared__ int32_t mine;
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const int i0 = wave * 64 * PER + lane;
+      int64_t t[PER];
+      uint64_t in[PER];
+      int sum = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) t[k] = i0 + 64 * k < a.n ? target_of(a, i0 + 64 * k) : -1;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        in[k] = __ballot(i0 + 64 * k < a.n && counted(a, t[k]));
+        sum += __popcll(in[k]);
+      }
+      if (lane == 0) part[wave] = sum;
+      __syncthreads();
+      int at = 0, count = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (w < wave) at += part[w];
+        count += part[w];
+      }
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int i = i0 + 64 * k, to = at + __popcll(in[k] & ((1ull << lane) - 1));
+        if ((in[k] >> lane) & 1) {
+          if (to == b) mine = i;
+          if (b == 0) {
+            a.perm[to] = i;
+            a.tgt[to] = (int32_t)t[k];
+          }
+        } else if (b == 0 && i < a.n && a.token_loss != nullptr) {
+          a.token_loss[i] = 0.f;
+        }
+        at += __popcll(in[k]);
+      }
+      if (b == 0 && threadIdx.x == 0) put_scalars(a, count);
+      __syncthreads();
+      ok = b < count;
+      token = ok ? mine : 0;
+    } else {
+      ok = b < a.sc->count;
+      token = ok ? a.perm[b] : 0;
+    }
+    const uint16_t* const src = a.x + token * a.width;
     for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8) copy_chunk(src, ok, a.width, c, a.xp + b * a.wpad);
     return;
   }
@@ -809,37 +867,36 @@ __global__ __launch_bounds__(256) void k_xent_transpose(const XentArgs a) {
   }
 }
 
-// lse and loss of each counted token from its tiles' statistics.
-__global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
-  // 32 tokens a block; 8 threads share a token's tiles
-  __shared__ float2 sh[8][32];
-  const int tl = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const int64_t ci = (int64_t)blockIdx.x * 32 + tl;
-  const int count = a.sc->count;
-  if ((int64_t)blockIdx.x * 32 >= count) return;
+// lse and loss of a counted token from its tiles' statistics.  32 tokens by 8
+// threads each; every thread of the workgroup calls it (ci may be past the
+// tokens).  The thread with part 0 returns the loss.
+__device__ __forceinline__ float token_lse(const XentArgs& a, int64_t ci, int count, int part, int tl,
+                                           float2 (*sh)[32]) {
   const int64_t tiles = a.rpad / kXTile;
   float m = -INFINITY, s = 0.f;
   constexpr int U = 8;  // tiles in flight
-  for (int64_t k0 = part; k0 < tiles; k0 += 8 * U) {
-    float2 q[U];
+  if (ci < count)
+    for (int64_t k0 = part; k0 < tiles; k0 += 8 * U) {
+      float2 q[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) q[u] = a.stats[min(k0 + 8 * u, tiles - 1) * a.npad + ci];
-    float nm = m;
+      for (int u = 0; u < U; ++u) q[u] = a.stats[min(k0 + 8 * u, tiles - 1) * a.npad + ci];
+      float nm = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k0 + 8 * u >= tiles) q[u] = make_float2(-INFINITY, 0.f);
-      nm = fmaxf(nm, q[u].x);
+      for (int u = 0; u < U; ++u) {
+        if (k0 + 8 * u >= tiles) q[u] = make_float2(-INFINITY, 0.f);
+        nm = fmaxf(nm, q[u].x);
+      }
+      // nothing finite so far: the sums are 0, or a NaN to pass on
+      const float b = nm == -INFINITY ? 0.f : nm;
+      s *= __builtin_amdgcn_exp2f((m - b) * kLog2e);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        s += q[u].x == -INFINITY ? q[u].y : q[u].y * __builtin_amdgcn_exp2f((q[u].x - b) * kLog2e);
+      m = nm;
     }
-    // nothing finite so far: the sums are 0, or a NaN to pass on
-    const float b = nm == -INFINITY ? 0.f : nm;
-    s *= __builtin_amdgcn_exp2f((m - b) * kLog2e);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      s += q[u].x == -INFINITY ? q[u].y : q[u].y * __builtin_amdgcn_exp2f((q[u].x - b) * kLog2e);
-    m = nm;
-  }
   sh[part][tl] = make_float2(m, s);
   __syncthreads();
+  float loss = 0.f;
   if (part == 0 && ci < count) {
     float mm = sh[0][tl].x;
 #pragma unroll
@@ -852,17 +909,16 @@ __global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
     }
     const float l = mm + logf((float)t);
     a.lse[ci] = l;
-    const float loss = l - a.tlogit[ci];
-    a.tlogit[ci] = loss;  // summed by k_xent_total
+    loss = l - a.tlogit[ci];
     if (a.token_loss != nullptr) a.token_loss[a.perm[ci]] = loss;
   }
+  __syncthreads();
+  return loss;
 }
 
-__global__ __launch_bounds__(1024) void k_xent_total(const XentArgs a) {
+// The loss from each thread's sum, in a fixed order.
+__device__ __forceinline__ void put_loss(const XentArgs& a, double s, int count) {
   __shared__ double red[16];
-  const int count = a.sc->count;
-  double s = 0.0;
-  for (int i = threadIdx.x; i < count; i += 1024) s += (double)a.tlogit[i];
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -872,6 +928,34 @@ __global__ __launch_bounds__(1024) void k_xent_total(const XentArgs a) {
     for (int k = 0; k < 16; ++k) v += red[k];
     a.loss[0] = (float)(a.mean ? v / (double)max(count, 1) : v);
   }
+}
+
+__global__ __launch_bounds__(256) void k_xent_lse(const XentArgs a) {
+  __shared__ float2 sh[8][32];
+  const int count = a.sc->count;
+  if ((int64_t)blockIdx.x * 32 >= count) return;
+  const int tl = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int64_t ci = (int64_t)blockIdx.x * 32 + tl;
+  const float loss = token_lse(a, ci, count, part, tl, sh);
+  if (part == 0 && ci < count) a.tlogit[ci] = loss;  // summed by k_xent_total
+}
+
+__global__ __launch_bounds__(1024) void k_xent_total(const XentArgs a) {
+  const int count = a.sc->count;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += 1024) s += (double)a.tlogit[i];
+  put_loss(a, s, count);
+}
+
+// Both in one workgroup, 128 tokens at a time, for few statistics (below
+// kXSoloStats): one launch instead of two.
+__global__ __launch_bounds__(1024) void k_xent_loss(const XentArgs a) {
+  __shared__ float2 sh[4][8][32];
+  const int count = a.sc->count;
+  const int tl = threadIdx.x & 31, part = (threadIdx.x >> 5) & 7, g = threadIdx.x >> 8;
+  double s = 0.0;
+  for (int64_t c0 = 0; c0 < count; c0 += 128) s += (double)token_lse(a, c0 + 32 * g + tl, count, part, tl, sh[g]);
+  put_loss(a, s, count);
 }
 
 // dx: the splits' sums in order, scaled and rounded; ignored tokens get zeros.
@@ -887,16 +971,25 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
     token = a.perm[b];
   } else {
     token = b - a.n;
-    const int64_t v = a.id_bits == 32 ? (int64_t)gmem(reinterpret_cast<const int32_t*>(a.targets))[token]
-                                      : gmem(reinterpret_cast<const int64_t*>(a.targets))[token];
-    if (v >= 0 && v < a.rows && v != a.ignore_index) return;
+    if (counted(a, target_of(a, token))) return;
     zero = true;
   }
   const float g = a.sc->gscale;
   for (int64_t c = threadIdx.x * 8; c < a.width; c += 256 * 8) {
     float e[8] = {};
     if (!zero) {
-      for (int k = 0; k < splits; ++k) {
+      constexpr int U = 8;  // parts in flight
+      int k = 0;
+      for (; k + U <= splits; k += U) {
+        float q[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load8(a.dxacc, ((int64_t)(k + u) * a.npad + b) * a.wpad + c, q[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) e[x] += q[u][x];
+      }
+      for (; k < splits; ++k) {
         float q[8];
         load8(a.dxacc, ((int64_t)k * a.npad + b) * a.wpad + c, q);
 #pragma unroll
@@ -916,12 +1009,14 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
 }  // namespace
 
 hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w_in, hipStream_t s) {
-  hipLaunchKernelGGL(k_xent_index, dim3(1), dim3(kIndexThreads), 0, s, a);
+  const bool list = a.n <= kXListTokens;
+  if (!list) hipLaunchKernelGGL(k_xent_index, dim3(1), dim3(kIndexThreads), 0, s, a);
   // the whole of w where its rows are no operand as they stand, else its last tile
   const int64_t w0 = copy_w ? 0 : a.wfull;
   uint16_t* const w_out = const_cast<uint16_t*>(copy_w ? a.w : a.wtail);
   const int64_t wrows = copy_w ? a.rpad : a.rpad - a.wfull;
-  hipLaunchKernelGGL(k_xent_gather, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
+  if (list) hipLaunchKernelGGL(k_xent_gather<true>, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
+  else hipLaunchKernelGGL(k_xent_gather<false>, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
   if (a.dw != nullptr)
     hipLaunchKernelGGL(k_xent_transpose, dim3(a.npad / 64, a.wpad / 64), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -942,6 +1037,10 @@ hipError_t launch_xent_stats(const XentArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_xent_loss(const XentArgs& a, hipStream_t s) {
+  if (a.n * (a.rpad / kXTile) <= kXSoloStats) {
+    hipLaunchKernelGGL(k_xent_loss, dim3(1), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_xent_lse, dim3(a.npad / 32), dim3(256), 0, s, a);
   hipLaunchKernelGGL(k_xent_total, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();

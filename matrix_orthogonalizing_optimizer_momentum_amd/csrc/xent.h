@@ -8,6 +8,8 @@ namespace muonh {
 
 constexpr int kXTile = 256;          // output tile side of the products
 constexpr int kXStage = 64;          // depth of one operand stage
+constexpr int64_t kXListTokens = 1024; // up to these, the list of counted tokens needs no launch of its own
+constexpr int64_t kXSoloStats = 16384; // statistics (128 KiB) that one workgroup turns into the loss
 constexpr int kXCus = 256;            // compute units, a multiple of the 8 XCDs
 // Parts that dx is summed in: many at few tokens, where dx has few tiles and
 // each is as deep as a piece (256 tokens, 50257 words, width 768: 224 us with up

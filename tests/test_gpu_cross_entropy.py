@@ -253,3 +253,15 @@ def test_gradients_against_differences():
             # P and the result are each within 2^-8 of their values; the directions' signs do not favour any
             slack = 2 * RB * (grad.double().cpu() * v).norm() + 1e-6
             assert abs(float(d - got)) <= float(slack) * 4
+
+
+@pytest.mark.parametrize("n,rows,width", [(1024, 259, 64), (1025, 259, 64), (1365, 3070, 64), (1366, 3070, 72), (5000, 1500, 64)])
+def test_both_sides_of_the_size_rules(n, rows, width):
+    # tokens listed by the gathering blocks (up to 1024) or by a launch of their
+    # own; loss by one workgroup (tokens x tiles up to 16384) or by many
+    print(f"[case] xent sizes {n} {rows} {width}", flush=True)
+    x, w, t = make(n, rows, width, 18)
+    check(x, w, t)
+    ok = (t >= 0) & (t < rows)
+    only = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
+    assert bool((only[1].cpu()[~ok] == 0).all())
