@@ -115,19 +115,20 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_sumsq(const GradTab tab, 
   }
 }
 
-// One workgroup: wave w sums the partials of tensors w, w + 16, ... (each lane
-// a fixed stride of them), then the waves' totals are added in order.  Lists
-// of ordinary length are staged in LDS first, with one trip to memory for all.
+// One workgroup: group g of 16 lanes sums the partials of tensors g, g + 64, ...
+// (each lane a fixed stride of them), then the groups' totals are added in
+// order.  Lists of ordinary length are staged in LDS first, with one trip to
+// memory for all.
 constexpr int kStagePartials = 4096, kStageTensors = 2047;
 __global__ __launch_bounds__(1024) void k_grad_finish(const double* __restrict__ partials,
                                                       const int32_t* __restrict__ bounds, int n, int nparts,
                                                       float max_norm, float* __restrict__ total,
                                                       float* __restrict__ coef, float* __restrict__ norms) {
-  constexpr int NW = 16;
-  __shared__ double red[NW];
+  constexpr int NW = 16, NG = 64, GL = 16;  // waves; groups and lanes of one
+  __shared__ double red[NG];
   __shared__ double part[kStagePartials];
   __shared__ int32_t first[kStageTensors + 1];
-  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int g = threadIdx.x / GL, l = threadIdx.x % GL;
   const bool staged = nparts <= kStagePartials && n <= kStageTensors;
   if (staged) {
     for (int i = threadIdx.x; i < nparts; i += 64 * NW) part[i] = gmem(partials)[i];
@@ -137,26 +138,26 @@ __global__ __launch_bounds__(1024) void k_grad_finish(const double* __restrict__
   auto bound = [&](int t) { return t >= n ? nparts : staged ? first[t] : gmem(bounds)[t]; };
   auto value = [&](int p) { return staged ? part[p] : gmem(partials)[p]; };
   double mine = 0.0;
-  for (int t = w; t < n; t += NW) {
+  for (int t = g; t < n; t += NG) {
     const int p0 = bound(t), p1 = bound(t + 1);
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     int p = p0 + l;
-    for (; p + 192 < p1; p += 256) {
+    for (; p + 3 * GL < p1; p += 4 * GL) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] += value(p + 64 * k);
+      for (int k = 0; k < 4; ++k) s[k] += value(p + GL * k);
     }
-    for (; p < p1; p += 64) s[0] += value(p);
-    const double v = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+    for (; p < p1; p += GL) s[0] += value(p);
+    double v = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = GL / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, GL);
     mine += v;
     if (l == 0 && norms != nullptr) gmem(norms)[t] = (float)sqrt(v);
   }
-  if (l == 0) red[w] = mine;
+  if (l == 0) red[g] = mine;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double v = 0.0;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) v += red[k];
-    const double tot = sqrt(v);
+  if (threadIdx.x < NG) {
+    const double tot = sqrt(wave_sum(red[threadIdx.x]));
+    if (threadIdx.x > 0) return;
     gmem(total)[0] = (float)tot;
     if (coef != nullptr) {
       const double c = (double)max_norm / (tot + 1e-6);

@@ -333,14 +333,6 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
   for (int j = 0; j < NI; ++j) bb[j] = frag_base<false>(wn * WN + j * 32, lane);
   f32x16_t acc[MI][NI];
-  auto clear = [&] {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  };
   bf16x8_t fa[2][MI], fb[2][NI];
   auto read_half = [&](int buf, int h) {
     const uint16_t* sa = reinterpret_cast<const uint16_t*>(smem + buf * 2 * kOperandB);
@@ -354,15 +346,16 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     }
   };
   // a half stage's 16 MFMAs, LOAD: with this wave's loads of the next stage
-  // (from src, into buffer buf) in between
-  auto mma_half = [&](auto load_c, const char* src, int buf) {
-    constexpr bool LOAD = decltype(load_c)::value;
+  // (from src, into buffer buf) in between; FIRST: of a tile, from zero
+  auto mma_half = [&](auto load_c, auto first_c, const char* src, int buf) {
+    constexpr bool LOAD = decltype(load_c)::value, FIRST = decltype(first_c)::value;
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int t = 0; t < 2 * MI * NI; ++t) {
       const int k = t / (MI * NI), i = (t / NI) % MI, j = t % NI;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[k][i], fb[k][j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[k][i], fb[k][j],
+                                                          FIRST && k == 0 ? f32x16_t{} : acc[i][j], 0, 0, 0);
       if (t & 1) {
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (LOAD) load_run(src, buf, t / 2);
@@ -432,14 +425,13 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
       for (int j = 0; j < NI; ++j) {
         const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
         const bool in = ci < count;
-        const float lb = in ? a.lse[ci] * kLog2e : 0.f;
+        const float lb = in ? a.lse[ci] * kLog2e : INFINITY;  // no token: weights of 0
         const int t = rel(in ? a.tgt[ci] : -1);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
-            acc[i][j][v] = in ? x : 0.f;
+            acc[i][j][v] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
           }
         // - 1 at the target, where this wave holds any token's
         if (__ballot(t != -64)) {
@@ -509,9 +501,8 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   // After its last tile a workgroup loads that tile's first stage once more,
   // to no use, which keeps the loop free of branches around the loads.
   const char* nsrc;
-  const std::true_type load{};
-  const std::false_type no_load{};
-  clear();
+  const std::true_type load{}, first{};
+  const std::false_type no_load{}, more{};
   load_stage(src, 0);
   wait_loads();
   barrier();
@@ -529,19 +520,20 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
         read_half(buf, 0);
         wait_lds();
         barrier();
-        mma_half(load, s + 1 < nstage ? src + (s + 1) * (kXStage * 2) : nsrc, buf ^ 1);
+        const char* const ld = s + 1 < nstage ? src + (s + 1) * (kXStage * 2) : nsrc;
+        if (s == 0) mma_half(load, first, ld, buf ^ 1);
+        else mma_half(load, more, ld, buf ^ 1);
         barrier();
         read_half(buf, 1);
         wait_lds();
         barrier();
-        mma_half(no_load, src, 0);
+        mma_half(no_load, more, src, 0);
         wait_loads();
         barrier();
         buf ^= 1;
       }
       epilogue(tok0, v0);
       if (next >= end) break;
-      clear();
       job = next;
       tok0 = ntok0;
       v0 = nv0;
@@ -559,19 +551,17 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
       }
       for (int s = 0; s < nstage; ++s) {
         const char* const ld = s + 1 < nstage ? src + (s + 1) * (kXStage * 2) : nsrc;
-        if (s > 0 || ptok0 >= 0) mma_half(load, ld, buf ^ 1);
+        if (s > 0 || ptok0 >= 0) mma_half(load, more, ld, buf ^ 1);
         else load_stage(ld, buf ^ 1);
-        if (s == 0 && ptok0 >= 0) {
-          epilogue(ptok0, pv0);
-          clear();
-        }
+        if (s == 0 && ptok0 >= 0) epilogue(ptok0, pv0);
         barrier();
         if (s == 0 && ptok0 >= 0) join(ptok0, pv0);
         __builtin_amdgcn_sched_barrier(0);
         read_half(buf, 0);
         wait_lds();
         barrier();
-        mma_half(no_load, src, 0);
+        if (s == 0) mma_half(no_load, first, src, 0);
+        else mma_half(no_load, more, src, 0);
         barrier();
         read_half(buf, 1);
         wait_lds();
@@ -587,7 +577,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
       v0 = nv0;
       src = nsrc;
     }
-    mma_half(no_load, src, 0);
+    mma_half(no_load, more, src, 0);
     epilogue(ptok0, pv0);
     if constexpr (STATS) {
       __syncthreads();
