@@ -424,15 +424,22 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         const int64_t ci = tok0 + wn * WN + j * 32 + (lane & 31);
-        const bool in = ci < count;
-        const float lb = in ? a.lse[ci] * kLog2e : INFINITY;  // no token: weights of 0
+        const int left = count - (int)tok0 - wn * WN - j * 32;  // tokens of these 32 rows
+        const bool in = (lane & 31) < left;
+        const float lb = in ? a.lse[ci] * kLog2e : 0.f;
         const int t = rel(in ? a.tgt[ci] : -1);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            acc[i][j][v] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
-          }
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, -lb));
+        // Rows of no token, in the last tile only, have weights of 0, also where
+        // an infinite w makes their logits (0 times w) NaN.
+        if (left < 32) {
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = in ? acc[i][j][v] : 0.f;
+        }
         // - 1 at the target, where this wave holds any token's
         if (__ballot(t != -64)) {
 #pragma unroll
@@ -443,7 +450,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
         // Through LDS (chunks of 8 words, swizzled by token against bank
         // conflicts), so that every store covers whole 128-byte lines, and past
         // the caches, which P (up to 512 MiB) would only sweep: at 8192 tokens,
-        // 50257 words, width 768 this kernel takes 632 us, with stores of 32
+        // 50257 words, width 768 this kernel takes 631 us, with stores of 32
         // bytes a row 682; the products that read P 1183, 1267.  (The same for
         // dw and dx's sums gained nothing.)
         char* const own = smem + kXSmem + wv * 4096;

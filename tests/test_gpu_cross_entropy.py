@@ -265,3 +265,31 @@ def test_both_sides_of_the_size_rules(n, rows, width):
     ok = (t >= 0) & (t < rows)
     only = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
     assert bool((only[1].cpu()[~ok] == 0).all())
+
+
+@pytest.mark.parametrize("n", [1, 37, 300, 1100])
+def test_words_shut_out_by_an_infinite_weight(n):
+    """A word whose logits are all -inf has weight 0 everywhere: the loss and
+    the other words' gradients are those without it, and its own is zero, whatever
+    stands behind the last token."""
+    print(f"[case] xent infinite weight, {n} tokens", flush=True)
+    x, w, t = make(n, 600, 128, 21)
+    x[:, 5] = 1.0
+    shut = [17, 300, 599]
+    t[torch.isin(t, torch.tensor(shut))] = 0
+    ok = (t >= 0) & (t < 600)
+    c = 1.0 / max(1, int(ok.sum()))
+    keep = torch.ones(600, dtype=torch.bool)
+    keep[shut] = False
+    place = torch.cumsum(keep, 0) - 1
+    small = torch.where(ok, place[t.clamp(0, 599)], 0)
+    loss, tol_loss, _, _, dw, tol_dw = reference(torch.where(ok[:, None], x, torch.zeros((), dtype=BF16)), w[keep],
+                                                 small, c, ok)
+    w[shut, 5] = -math.inf
+    got, tok, gx, gw = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad="w", dw_dtype=F32)
+    assert gx is None
+    assert bool(((tok.double().cpu() - loss).abs() <= tol_loss).all())
+    assert abs(float(got) - float(loss.sum()) * c) <= float(tol_loss.sum()) * c + ULP32 * abs(float(got))
+    assert bool((gw.cpu()[~keep] == 0).all())
+    e = (gw.double().cpu()[keep] - dw).abs()
+    assert bool((e <= tol_dw + ULP32 * dw.abs()).all()), float((e - tol_dw).max())
