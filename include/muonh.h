@@ -423,7 +423,7 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
  * returned when the limit is below the smallest piece's need, or for invalid
  * sizes; only the address of w matters, its alignment).  A row of w that is
  * not a multiple of 64 values, or not on a 16-byte grid, is copied to the
- * workspace once.
+ * workspace once (not for the loss alone of up to 64 tokens).
  */
 enum { MUONH_REDUCE_MEAN = 0, MUONH_REDUCE_SUM = 1 };
 size_t muonh_cross_entropy_workspace(const void* w, int64_t n, int64_t rows, int64_t width, int grads, size_t limit);

@@ -160,7 +160,7 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t width) {
 // ------------------------------------------------------------ cross entropy
 // Scratch of one call: what every call needs, then what the gradients need.
 struct XentPlan {
-  bool copy_w;
+  bool few, copy_w;
   int64_t npad, rpad, wpad, wfull, ldxt, cols, splits;
   int64_t sc, xp, xt, perm, tgt, lse, tlogit, wcopy, area, dxacc, bytes;
 };
@@ -259,6 +259,13 @@ XentPlan xent_layout(const void* w, int64_t n, int64_t rows, int64_t width, bool
 int xent_plan(const void* w, int64_t n, int64_t rows, int64_t width, bool dx, bool dw, int64_t limit, XentPlan& p) {
   const int64_t npad = up(std::max<int64_t>(n, 1), kXTile), rpad = up(rows, kXTile);
   if (!dx && !dw) {
+    if (n <= kXFewTokens && width >= 8) {
+      p = XentPlan{};
+      p.few = true;
+      p.area = up(4 * kXFewTokens, 256);  // behind the targets' logits
+      p.bytes = p.area + up(8 * n * xent_few_blocks(rows), 256);
+      return p.bytes <= limit ? MUONH_OK : MUONH_ENOMEM;
+    }
     p = xent_layout(w, n, rows, width, false, false, 0, 1);
     return p.bytes <= limit ? MUONH_OK : MUONH_ENOMEM;
   }
@@ -489,6 +496,11 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
   a.dw_dt = internal_dtype(dw_dtype);
   a.accumulate = accumulate;
   const double mac = 2.0 * (double)n * (double)rows * (double)width;
+  if (p.few) {
+    ProfScope pf(s, PC_XLOGIT, mac, 0);
+    MUONH_TRY_HIP(launch_xent_few(a, s));
+    return MUONH_OK;
+  }
   {
     ProfScope pf(s, PC_XPREP, 0, 4.0 * (double)p.npad * (double)p.wpad);
     MUONH_TRY_HIP(launch_xent_prepare(a, p.copy_w, static_cast<const uint16_t*>(w), s));

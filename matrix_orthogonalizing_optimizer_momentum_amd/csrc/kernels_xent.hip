@@ -1003,6 +1003,245 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// few tokens, loss only: up to kXFewTokens
+// ---------------------------------------------------------------------------
+// Tiles of 256 tokens would be nearly empty, and the time is that of reading w
+// once.  Here a wave is a workgroup and takes 64 words and 32 NT tokens at a
+// time.  It reads whole 128-byte runs of rows, at any alignment (w needs no
+// padded copy), two stages of 64 values ahead into registers, and passes them through
+// its own LDS to the fragments' layout: nothing waits for another wave.  Bound
+// by HBM: 17 us for 50257 x 768 (4.6 TB/s), 128 for 151936 x 2048 (4.9).  Reads
+// straight into the fragments' layout (32 rows an instruction) took 22 and 190.
+// A token stands in its own column, so what an uncounted one holds stays there.
+__device__ __forceinline__ void wave_fence() {  // orders a wave's LDS accesses, which execute in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int NT>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_few(const XentArgs a,
+                                                                                         int blocks) {
+  constexpr int MW = kXFewWords / 32, RW = kXFewWords / 8, RT = 4 * NT;  // runs of 8 rows of a stage
+  __shared__ __attribute__((aligned(16))) uint16_t tile[(kXFewWords + 32 * NT) * kXStage];
+  const int lane = threadIdx.x, hi = lane >> 5;
+  const int64_t units = (a.width + kXStage - 1) / kXStage;
+  const int64_t tiles = (a.rows + kXFewWords - 1) / kXFewWords;
+  const int64_t mine = (tiles - (int64_t)blockIdx.x + blocks - 1) / blocks;
+  const int64_t stages = mine * units;
+  // 8 lanes a row; a lane's chunk of 8 values, as swizzled in LDS
+  const int r8 = lane >> 3;
+  int col[2];  // chunks of even and odd runs differ: swz of rows 8 apart
+#pragma unroll
+  for (int e = 0; e < 2; ++e) col[e] = 8 * ((lane & 7) ^ swz(8 * e + r8));
+  uint32_t offw[RW], offt[RT];  // of the rows, from their tile's first one, in elements
+#pragma unroll
+  for (int p = 0; p < RT; ++p) offt[p] = (uint32_t)(min<int64_t>(8 * p + r8, a.n - 1) * a.width);
+  // the next stage to load
+  int64_t lv = (int64_t)blockIdx.x * kXFewWords, lu = 0;
+  auto rows_of = [&]() {
+#pragma unroll
+    for (int p = 0; p < RW; ++p) offw[p] = (uint32_t)((min<int64_t>(lv + 8 * p + r8, a.rows - 1) - lv) * a.width);
+  };
+  rows_of();
+  struct Stage {
+    u32x4_t w[RW], t[RT];
+  };
+  // A lane's chunk that ends behind its row is read from the row's end, and
+  // moved into place before it is used.
+  auto fetch = [&](Stage& q) {
+    const int64_t c = lu * kXStage;
+    const int last = (int)min<int64_t>(a.width - c, kXStage) - 8;  // may be below 0: widths are 8 at least
+    const uint16_t* const bw = a.w + lv * a.width + c;
+    const uint16_t* const bt = a.x + c;
+    const int c0 = min(col[0], last), c1 = min(col[1], last);
+#pragma unroll
+    for (int p = 0; p < RW; ++p)
+      q.w[p] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(bw) + ((int64_t)offw[p] + (p & 1 ? c1 : c0)));
+#pragma unroll
+    for (int p = 0; p < RT; ++p)
+      q.t[p] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(bt) + ((int64_t)offt[p] + (p & 1 ? c1 : c0)));
+    // on to the next; after the last one the first of this tile again, to no use
+    if (++lu == units) {
+      lu = 0;
+      if (lv + (int64_t)blocks * kXFewWords < a.rows) {
+        lv += (int64_t)blocks * kXFewWords;
+        rows_of();
+      }
+    }
+  };
+  int64_t t[NT];
+  float m[NT], s[NT];  // running maximum and sum of this lane's words, by token
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int token = 32 * j + (lane & 31);
+    t[j] = token < a.n ? target_of(a, token) : -1;
+    m[j] = -INFINITY;
+    s[j] = 0.f;
+  }
+  f32x16_t acc[NT][MW];
+  int64_t v0 = lv, u = 0;  // the stage in hand
+  const int short_last = (int)(a.width - (units - 1) * kXStage) - 8;  // of the last stage
+  auto shift = [](u32x4_t& q, int by) {  // by values down, zeros from above; by = 8: all zeros
+    uint64_t lo = (uint64_t)q[1] << 32 | q[0], up = (uint64_t)q[3] << 32 | q[2];
+    const int b = 16 * (by & 3);
+    if (by >= 4) {
+      lo = by >= 8 ? 0 : up >> b;
+      up = 0;
+    } else if (by > 0) {
+      lo = lo >> b | up << (64 - b);
+      up >>= b;
+    }
+    q = u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)up, (uint32_t)(up >> 32)};
+  };
+  auto work = [&](Stage& q, bool ahead) {
+    if (u == units - 1 && short_last < kXStage - 8) {
+      const int by0 = min(max(col[0] - short_last, 0), 8), by1 = min(max(col[1] - short_last, 0), 8);
+#pragma unroll
+      for (int p = 0; p < RW; ++p) shift(q.w[p], p & 1 ? by1 : by0);
+#pragma unroll
+      for (int p = 0; p < RT; ++p) shift(q.t[p], p & 1 ? by1 : by0);
+    }
+    wave_fence();
+#pragma unroll
+    for (int p = 0; p < RW; ++p) *reinterpret_cast<u32x4_t*>(tile + p * 512 + lane * 8) = q.w[p];
+#pragma unroll
+    for (int p = 0; p < RT; ++p) *reinterpret_cast<u32x4_t*>(tile + (RW + p) * 512 + lane * 8) = q.t[p];
+    wave_fence();
+    if (ahead) fetch(q);
+    if (u == 0) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MW; ++i) acc[j][i] = f32x16_t{};
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int xk = ((2 * k + hi) ^ swz(lane & 31)) * 8;
+      bf16x8_t fa[MW], fb[NT];
+#pragma unroll
+      for (int i = 0; i < MW; ++i) fa[i] = frag<false>(tile, frag_base<false>(32 * i, lane), xk, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[j] = frag<false>(tile, frag_base<false>(kXFewWords + 32 * j, lane), xk, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MW; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[j][i], 0, 0, 0);
+    }
+    if (++u < units) return;
+    // the tile's logits are complete
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int token = 32 * j + (lane & 31);
+      const int64_t tr = t[j] - v0 - 4 * hi;  // the target, counted as below
+      const int own = tr >= 0 && tr < kXFewWords ? (int)tr : -1;
+      const int words = (int)min<int64_t>(a.rows - v0, kXFewWords) - 4 * hi;
+      float nm = m[j];
+#pragma unroll
+      for (int i = 0; i < MW; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int word = 32 * i + 8 * (v >> 2) + (v & 3);
+          if (word >= words) acc[j][i][v] = -INFINITY;
+          if (word == own) a.tlogit[token] = acc[j][i][v];
+          nm = fmaxf(nm, acc[j][i][v]);
+        }
+      // nothing finite so far: the sums are 0, or a NaN to pass on
+      const float b = nm == -INFINITY ? 0.f : nm * kLog2e;
+      s[j] *= __builtin_amdgcn_exp2f(fmaf(m[j], kLog2e, -b));
+#pragma unroll
+      for (int i = 0; i < MW; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[j] += __builtin_amdgcn_exp2f(fmaf(acc[j][i][v], kLog2e, -b));
+      m[j] = nm;
+    }
+    u = 0;
+    v0 += (int64_t)blocks * kXFewWords;
+  };
+  Stage q0;
+  fetch(q0);
+  if constexpr (NT == 1) {
+    Stage q1;
+    fetch(q1);
+    for (int64_t g = 0; g < stages; g += 2) {
+      work(q0, g + 2 < stages);
+      if (g + 1 < stages) work(q1, g + 3 < stages);
+    }
+  } else {  // registers for one stage ahead
+    for (int64_t g = 0; g < stages; ++g) work(q0, g + 1 < stages);
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int token = 32 * j + (lane & 31);
+    const float m1 = __shfl_xor(m[j], 32, 64), s1 = __shfl_xor(s[j], 32, 64);
+    const float mm = fmaxf(m[j], m1), b = mm == -INFINITY ? 0.f : mm * kLog2e;
+    const float sum = s[j] * __builtin_amdgcn_exp2f(fmaf(m[j], kLog2e, -b)) +
+                      s1 * __builtin_amdgcn_exp2f(fmaf(m1, kLog2e, -b));
+    if (hi == 0 && token < a.n) a.stats[(int64_t)token * blocks + blockIdx.x] = make_float2(mm, sum);
+  }
+}
+
+// Their losses, a wave a token.
+__global__ __launch_bounds__(1024) void k_xent_few_loss(const XentArgs a, int blocks) {
+  __shared__ double red[16];
+  __shared__ int cnt[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double sum = 0.0;
+  int count = 0;
+  for (int token = wave; token < a.n; token += 16) {
+    if (!counted(a, target_of(a, token))) {
+      if (lane == 0 && a.token_loss != nullptr) a.token_loss[token] = 0.f;
+      continue;
+    }
+    const float tl = a.tlogit[token];
+    float m = -INFINITY, s = 0.f;
+    constexpr int U = 8;  // statistics in flight, a lane
+    for (int b0 = lane; b0 - lane < blocks; b0 += 64 * U) {
+      float2 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) q[u] = a.stats[(int64_t)token * blocks + min(b0 + 64 * u, blocks - 1)];
+      float nm = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b0 + 64 * u >= blocks) q[u] = make_float2(-INFINITY, 0.f);
+        nm = fmaxf(nm, q[u].x);
+      }
+      // nothing finite so far: the sums are 0, or a NaN to pass on
+      const float b = nm == -INFINITY ? 0.f : nm * kLog2e;
+      s *= __builtin_amdgcn_exp2f(fmaf(m, kLog2e, -b));
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += q[u].y * __builtin_amdgcn_exp2f(fmaf(q[u].x, kLog2e, -b));
+      m = nm;
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    s *= __builtin_amdgcn_exp2f(fmaf(m, kLog2e, top == -INFINITY ? 0.f : -top * kLog2e));
+    m = top;
+    const double all = wave_sum((double)s);
+    const float loss = m + logf((float)all) - tl;
+    if (lane == 0 && a.token_loss != nullptr) a.token_loss[token] = loss;
+    sum += (double)loss;
+    ++count;
+  }
+  if (lane == 0) {
+    red[wave] = sum;
+    cnt[wave] = count;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      v += red[k];
+      c += cnt[k];
+    }
+    a.loss[0] = (float)(a.mean ? v / (double)max(c, 1) : v);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w_in, hipStream_t s) {
@@ -1024,6 +1263,14 @@ hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w
 static int logit_blocks(const XentArgs& a, int nvoc) {
   const int64_t jobs = a.npad / kXTile * nvoc;
   return (int)(jobs < kXCus ? (jobs + 7) / 8 * 8 : kXCus);
+}
+
+hipError_t launch_xent_few(const XentArgs& a, hipStream_t s) {
+  const int blocks = xent_few_blocks(a.rows);
+  if (a.n > 32) hipLaunchKernelGGL(k_xent_few<2>, dim3(blocks), dim3(64), 0, s, a, blocks);
+  else if (a.n > 0) hipLaunchKernelGGL(k_xent_few<1>, dim3(blocks), dim3(64), 0, s, a, blocks);
+  hipLaunchKernelGGL(k_xent_few_loss, dim3(1), dim3(1024), 0, s, a, blocks);
+  return hipGetLastError();
 }
 
 hipError_t launch_xent_stats(const XentArgs& a, hipStream_t s) {

@@ -18,6 +18,21 @@ constexpr int kXMaxSplits = 64;
 constexpr int64_t kXSplitBytes = (int64_t)256 << 20;
 constexpr int64_t kXMaxWidth = 65536, kXMaxTokens = (int64_t)1 << 22, kXMaxRows = (int64_t)1 << 23;
 
+// The loss of up to kXFewTokens tokens without gradients (rows of w of 8 values
+// at least) has kernels of its own, that take 64 words at a time in at most
+// kXFewBlocks workgroups.  Against tiles of 256 tokens: 17 tokens, 50257 x 768
+// 33 -> 23 us, 64 tokens 34 -> 33; 151936 x 2048, 8 tokens 195 -> 136, 64 tokens
+// 194 -> 157; 3 tokens, 141353 x 221, where the tiles need a copy of w, 101 -> 24.
+constexpr int64_t kXFewTokens = 64;
+constexpr int kXFewWords = 64, kXFewBlocks = 2048;
+// Workgroups (of one wave, all resident at once), with the same number of
+// rounds each.
+inline int xent_few_blocks(int64_t rows) {
+  const int64_t tiles = (rows + kXFewWords - 1) / kXFewWords;
+  const int64_t rounds = (tiles + kXFewBlocks - 1) / kXFewBlocks;
+  return (int)((tiles + rounds - 1) / rounds);
+}
+
 // Device scalars of one call.
 struct XentScalars {
   int32_t count;                     // counted tokens
@@ -34,8 +49,8 @@ struct XentArgs {
   int32_t* perm;                     // xp row -> token
   int32_t* tgt;                      // xp row -> target
   float* lse;                        // per xp row
-  float* tlogit;                     // per xp row: the target's logit
-  float2* stats;                     // [rows / kXTile][npad]: maximum and sum of exp per tile
+  float* tlogit;                     // per xp row (few tokens: per token): the target's logit
+  float2* stats;                     // [rows / kXTile][npad]: maximum and sum of exp per tile (few tokens: [n][blocks])
   uint16_t* prob;                    // npad x piece
   float* dxacc;                      // [splits][npad][wpad]
   XentScalars* sc;
@@ -59,6 +74,7 @@ struct XentPiece {
 };
 
 hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w_in, hipStream_t s);
+hipError_t launch_xent_few(const XentArgs& a, hipStream_t s);  // the whole call
 hipError_t launch_xent_stats(const XentArgs& a, hipStream_t s);
 hipError_t launch_xent_loss(const XentArgs& a, hipStream_t s);
 hipError_t launch_xent_prob(const XentArgs& a, const XentPiece& p, hipStream_t s);

@@ -293,3 +293,72 @@ def test_words_shut_out_by_an_infinite_weight(n):
     assert bool((gw.cpu()[~keep] == 0).all())
     e = (gw.double().cpu()[keep] - dw).abs()
     assert bool((e <= tol_dw + ULP32 * dw.abs()).all()), float((e - tol_dw).max())
+
+
+def check_loss(x, w, t, reduction="mean"):
+    """The loss alone, with the tolerance of `reference`."""
+    ok = (t >= 0) & (t < w.shape[0])
+    c = 1.0 / max(1, int(ok.sum())) if reduction == "mean" else 1.0
+    clean = torch.where(ok[:, None], x, torch.zeros((), dtype=BF16))
+    loss, tol, *_ = reference(clean, w, t, c, ok)
+    got, tok, gx, gw = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), reduction=reduction, grad=False)
+    assert gx is None and gw is None
+    e = (tok.double().cpu() - loss).abs()
+    assert bool((e <= tol).all()), float((e - tol).max())
+    assert bool((tok.cpu()[~ok] == 0).all())
+    assert abs(float(got) - float(loss.sum()) * c) <= float(tol.sum()) * c + ULP32 * abs(float(got))
+    return got, tok
+
+
+@pytest.mark.parametrize("n", [1, 5, 31, 32, 33, 64, 65])
+@pytest.mark.parametrize("rows,width", [(1, 1), (63, 7), (64, 64), (65, 63), (1000, 65), (5001, 320), (70000, 100)])
+def test_loss_of_few_tokens(n, rows, width):
+    print(f"[case] xent loss, {n} tokens, {rows} x {width}", flush=True)
+    x, w, t = make(n, rows, width, 31)
+    if n > 4:
+        t[4] = rows - 1
+        x[1] = math.inf  # not counted
+    check_loss(x, w, t, "sum" if n % 2 else "mean")
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_loss_of_few_tokens_off_the_grid(n):
+    print(f"[case] xent loss off the grid, {n}", flush=True)
+    x, w, t = make(n, 900, 130, 32)
+    want = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
+    got = mm.cross_entropy(_offset(x.to(DEV), 1), _offset(w.to(DEV), 3), _offset(t.to(DEV), 1), grad=False)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    # and as int32, on another stream, captured
+    s = torch.cuda.Stream()
+    X, W, T = x.to(DEV), w.to(DEV), t.to(DEV).int()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = mm.cross_entropy(X, W, T, grad=False)
+    for _ in range(3):
+        out[0].zero_(), out[1].fill_(-1.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+
+
+def test_loss_of_few_tokens_none_counted_and_not_finite():
+    print("[case] xent loss, none counted / not finite", flush=True)
+    x, w, t = make(6, 300, 96, 33, pad=False)
+    got = mm.cross_entropy(x.to(DEV), w.to(DEV), torch.full((6,), -100, device=DEV), grad=False)
+    assert float(got[0]) == 0 and bool((got[1] == 0).all())
+    got = mm.cross_entropy(x[:0].to(DEV), w.to(DEV), t[:0].to(DEV), grad=False)
+    assert float(got[0]) == 0 and got[1].numel() == 0
+    x[2, 7] = math.nan  # stays in its token
+    got = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
+    assert bool(got[1][2].isnan()) and bool(got[0].isnan())
+    assert bool(got[1].isfinite()[[0, 1, 3, 4, 5]].all())
+    # words shut out by an infinite weight
+    x, w, t = make(6, 300, 96, 34, pad=False)
+    x[:, 5] = 1.0
+    t[:] = torch.tensor([0, 1, 2, 3, 4, 5])
+    want = mm.cross_entropy(x.to(DEV), w[:100].contiguous().to(DEV), t.to(DEV), grad=False)
+    w[100:, 5] = -math.inf
+    got = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
+    # both are one sum of the same exponents, in two groupings
+    assert bool(((got[1] - want[1]).abs() <= 64 * ULP32 * (1 + want[1].abs())).all())
