@@ -1011,8 +1011,9 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
 // time.  It reads whole 128-byte runs of rows, at any alignment (w needs no
 // padded copy), two stages of 64 values ahead into registers, and passes them through
 // its own LDS to the fragments' layout: nothing waits for another wave.  Bound
-// by HBM: 17 us for 50257 x 768 (4.6 TB/s), 128 for 151936 x 2048 (4.9).  Reads
-// straight into the fragments' layout (32 rows an instruction) took 22 and 190.
+// by HBM: 17 us for 50257 x 768 (4.6 TB/s).  Reads straight into the fragments'
+// layout (32 rows an instruction), the depth split over four waves: 32 tokens 34
+// us a call against 25, at 151936 x 2048 234 against 140.
 // A token stands in its own column, so what an uncounted one holds stays there.
 __device__ __forceinline__ void wave_fence() {  // orders a wave's LDS accesses, which execute in order
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
