@@ -7,7 +7,7 @@
 // Both passes stream: the norm reads every gradient once, clipping reads it
 // again and writes it.  What the norm read stays in the last-level cache as far
 // as it fits; clipping reads and writes past the caches (non-temporal), so that
-// its results do not push out what it has yet to read (85 MB of bf16 values:
+// its results do not push out what it has yet to read (85 million bf16 values:
 // 110 -> 85 us with its norm).  Tensors' 16-byte grids are used for loads;
 // stores go to any alignment.  The list of tensors travels in the kernel arguments
 // (kTabTensors a launch), so a call uploads no table, keeps nothing between

@@ -684,7 +684,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int64_t d = d0 + wm * WM + i * 32 + 8 * q + 4 * hi;
-        if (d >= a.wpad) continue;
+        if (d >= a.wpad || ci >= count) continue;  // 64 tokens, 50257 x 768: 134 -> 127 us a call
         f32x4_t e = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         MUONH_GLOBAL f32x4_t* const o = reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(out + ci * a.wpad + d));
         if (!p.first) e += *o;
@@ -778,12 +778,13 @@ __device__ __forceinline__ void copy_chunk(const uint16_t* src, bool row_ok, int
 }
 
 // Blocks [0, npad): one row of xp each (counted tokens of x, then zeros); the
-// others: one row of the padded copy of the weights from row w0 on.  LIST: up
+// others: chunks of the padded copy of the weights, wrows rows from row w0 on.  LIST: up
 // to kXListTokens tokens, where every block finds its token itself and the
 // first one writes the list, which saves k_xent_index.
+constexpr int kCopyPer = 4;
 template <bool LIST>
 __global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uint16_t* w_in, uint16_t* w_out,
-                                                     int64_t w0) {
+                                                     int64_t w0, int64_t wrows) {
   const int64_t b = blockIdx.x;
   if (b < a.npad) {
     bool ok;
@@ -838,9 +839,23 @@ __global__ __launch_bounds__(256) void k_xent_gather(const XentArgs a, const uin
     for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8) copy_chunk(src, ok, a.width, c, a.xp + b * a.wpad);
     return;
   }
-  const int64_t r = b - a.npad, v = w0 + r;
-  for (int64_t c = threadIdx.x * 8; c < a.wpad; c += 256 * 8)
-    copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, c, w_out + r * a.wpad);
+  // kCopyPer chunks of 8 values a thread (a block a row took 63 us for 140788 x
+  // 103, this 16); a block's first row comes from one 64-bit division, a thread's
+  // from a 32-bit one
+  const uint32_t cpr = (uint32_t)(a.wpad / 8);
+  for (int64_t i0 = (b - a.npad) * (256 * kCopyPer); i0 < wrows * cpr;
+       i0 += (int64_t)(gridDim.x - a.npad) * (256 * kCopyPer)) {
+    const int64_t row0 = i0 / cpr;
+    const uint32_t off0 = (uint32_t)(i0 - row0 * cpr);
+#pragma unroll
+    for (int k = 0; k < kCopyPer; ++k) {
+      const uint32_t x = off0 + threadIdx.x + 256 * k, q = x / cpr;
+      const int64_t r = row0 + q, v = w0 + r;
+      if (r < wrows)
+        copy_chunk(w_in + min(v, a.rows - 1) * a.width, v < a.rows, a.width, 8 * (int64_t)(x - q * cpr),
+                   w_out + r * a.wpad);
+    }
+  }
 }
 
 // xt = xp transposed, 64 x 64 values a block.
@@ -1252,8 +1267,10 @@ hipError_t launch_xent_prepare(const XentArgs& a, bool copy_w, const uint16_t* w
   const int64_t w0 = copy_w ? 0 : a.wfull;
   uint16_t* const w_out = const_cast<uint16_t*>(copy_w ? a.w : a.wtail);
   const int64_t wrows = copy_w ? a.rpad : a.rpad - a.wfull;
-  if (list) hipLaunchKernelGGL(k_xent_gather<true>, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
-  else hipLaunchKernelGGL(k_xent_gather<false>, dim3(a.npad + wrows), dim3(256), 0, s, a, w_in, w_out, w0);
+  const int64_t copies = (wrows * (a.wpad / 8) + 256 * kCopyPer - 1) / (256 * kCopyPer);
+  const dim3 grid(a.npad + (copies < (1 << 20) ? copies : 1 << 20));
+  if (list) hipLaunchKernelGGL(k_xent_gather<true>, grid, dim3(256), 0, s, a, w_in, w_out, w0, wrows);
+  else hipLaunchKernelGGL(k_xent_gather<false>, grid, dim3(256), 0, s, a, w_in, w_out, w0, wrows);
   if (a.dw != nullptr)
     hipLaunchKernelGGL(k_xent_transpose, dim3(a.npad / 64, a.wpad / 64), dim3(256), 0, s, a);
   return hipGetLastError();
