@@ -356,9 +356,8 @@ int muonh_grad_norm(const void* const grads[], const int64_t numel[], const int 
 /*
  * muonh_clip_grads -- muonh_grad_norm, then outs[t] = coef * grads[t] in the
  * gradient's own dtype (one rounding).  outs[t] may be grads[t] (in place;
- * nothing is written when coef is 1), else the buffers must not overlap; a
- * buffer listed twice among outs is refused.  Workspace:
- * muonh_grad_norm_workspace(n).
+ * nothing is written when coef is 1); outs that overlap each other or another
+ * gradient are refused (MUONH_EINVAL).  Workspace: muonh_grad_norm_workspace(n).
  */
 int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_t numel[], const int dtypes[], int n,
                      float max_norm, float* total, float* coef, void* workspace, size_t workspace_bytes,

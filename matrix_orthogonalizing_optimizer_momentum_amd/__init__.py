@@ -284,6 +284,8 @@ def make_opts(state_dtype=MUONH_BF16, ns_dtype="bf16", ns_precision="h16", coeff
     if stream is None:
         import torch
         stream = torch.cuda.current_stream()
+    if grad_scale is not None and getattr(stream, "device", grad_scale.device) != grad_scale.device:
+        raise ValueError("grad_scale is on another device than the stream")
     o.stream = c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
     return o, keep
 

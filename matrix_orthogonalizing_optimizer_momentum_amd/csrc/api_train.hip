@@ -55,15 +55,31 @@ int check_grads(const void* const* grads, const int64_t* numel, const int* dtype
   return total > ((int64_t)1 << 50) ? MUONH_EINVAL : MUONH_OK;
 }
 
-// Whether a buffer is listed twice (writes to it would race).
-int check_distinct(void* const* outs, const int64_t* numel, int n) {
-  std::unique_ptr<uintptr_t[]> v(new (std::nothrow) uintptr_t[n]);
+// Clipping writes outs[i] while it reads grads: outs must not overlap each
+// other, nor a gradient other than their own, in place.
+int check_outs(const void* const* grads, void* const* outs, const int64_t* numel, const int* dtypes, int n) {
+  struct Span {
+    uintptr_t lo, hi;
+  };
+  std::unique_ptr<Span[]> v(new (std::nothrow) Span[n]);
   if (!v) return MUONH_ENOMEM;
+  auto span = [&](const void* p, int i) {
+    return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)grad_bytes(numel[i], dtypes[i])};
+  };
   int m = 0;
   for (int i = 0; i < n; ++i)
-    if (numel[i] > 0) v[m++] = (uintptr_t)outs[i];
-  std::sort(v.get(), v.get() + m);
-  return std::adjacent_find(v.get(), v.get() + m) == v.get() + m ? MUONH_OK : MUONH_EINVAL;
+    if (numel[i] > 0) v[m++] = span(outs[i], i);
+  Span* const end = v.get() + m;
+  std::sort(v.get(), end, [](const Span& x, const Span& y) { return x.lo < y.lo; });
+  for (int k = 1; k < m; ++k)
+    if (v[k].lo < v[k - 1].hi) return MUONH_EINVAL;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0 || grads[i] == outs[i]) continue;
+    const Span g = span(grads[i], i);
+    const Span* const o = std::partition_point(v.get(), end, [&](const Span& x) { return x.hi <= g.lo; });
+    if (o != end && o->lo < g.hi) return MUONH_EINVAL;
+  }
+  return MUONH_OK;
 }
 
 // The table of tensors [i0, i0 + t.n) and its number of blocks.
@@ -327,7 +343,7 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
   for (int i = 0; i < n; ++i)
     if (numel[i] > 0 && (!outs[i] || (uintptr_t)outs[i] % (dtypes[i] == MUONH_F32 ? 4 : 2) != 0)) return MUONH_EINVAL;
   if (!std::isfinite(max_norm) || max_norm < 0.f) return MUONH_EINVAL;
-  const int rd = check_distinct(outs, numel, n);
+  const int rd = check_outs(grads, outs, numel, dtypes, n);
   if (rd != MUONH_OK) return rd;
   if (workspace_bytes < muonh_grad_norm_workspace(n)) return MUONH_ENOMEM;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -287,6 +287,26 @@ def test_a_gradient_listed_twice():
         mm.clip_grads([g, g], 1.0)
 
 
+def test_clip_neighbouring_buffers():
+    """Views of one flat buffer, in place and into another one; one gradient twice."""
+    print("[case] clip neighbours", flush=True)
+    torch.manual_seed(5)
+    flat = torch.randn(1001, device=DEV) * 3
+    want = flat.double() / (flat.double().norm() + 1e-6)
+    cut = lambda t: [t[:3], t[3:500], t[500:]]  # noqa: E731
+    other = torch.empty_like(flat)
+    mm.clip_grads(cut(flat), 1.0, outputs=cut(other))
+    mm.clip_grads(cut(flat), 1.0)
+    # the coefficient and the product are rounded once each
+    assert bool(((flat.double() - want).abs() <= 2.0 ** -22 * want.abs()).all())
+    assert torch.equal(flat, other)
+    g, a, b = torch.ones(8, device=DEV), torch.empty(8, device=DEV), torch.empty(8, device=DEV)
+    mm.clip_grads([g, g], 2.0, outputs=[a, b])
+    assert torch.equal(a, b) and abs(float(a[0]) - 0.5) < 1e-6
+    with pytest.raises(mm.MuonhError):
+        mm.clip_grads([a, b], 1.0, outputs=[b, a])
+
+
 def test_python_refusals():
     print("[case] refusals", flush=True)
     t, i = torch.randn(6, 8, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)

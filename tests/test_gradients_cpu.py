@@ -180,3 +180,29 @@ def test_options_carry_the_scale():
     mm.load().muonh_default_opts(ctypes.byref(o))
     assert o.grad_scale is None
     assert ctypes.sizeof(mm.Opts) % 8 == 0 and mm.Opts.grad_scale.offset == ctypes.sizeof(mm.Opts) - 8
+
+
+@pytest.mark.parametrize("ptrs,outs", [
+    ((P, P + 256), (P + 256, P)),           # each the other's
+    ((P, P + 256), (P + 512, P + 528)),     # outs overlap: 8 float32 and 8 bfloat16
+    ((P, P + 256), (P + 16, P + 768)),      # its own gradient, not in place
+    ((P, P + 256), (P + 240, P + 768)),     # the next one's first values
+    ((P, P + 256), (P, P + 16)),            # in place, and inside the first
+])
+def test_clip_refuses_overlapping_buffers(ptrs, outs):
+    assert norm(True, ptrs=ptrs, outs=outs) == mm.MUONH_EINVAL
+    # behind the check of the workspace when they are apart
+    assert norm(True, ptrs=ptrs, outs=(P + 1024, P + 1056), ws_bytes=1) == mm.MUONH_ENOMEM
+    assert norm(True, ptrs=(P, P), outs=(P + 32, P + 64), ws_bytes=1) == mm.MUONH_ENOMEM
+    assert norm(True, ptrs=(P, P + 32), outs=(P, P + 32), ws_bytes=1) == mm.MUONH_ENOMEM
+    assert norm(True, ptrs=(P, P + 32), outs=(P, P + 64), numel=(8, 0), ws_bytes=1) == mm.MUONH_ENOMEM
+
+
+def test_grad_scale_of_another_device():
+    from types import SimpleNamespace
+    scale = SimpleNamespace(is_cuda=True, dtype=torch.float32, numel=lambda: 1, data_ptr=lambda: P,
+                            device=torch.device("cuda:1"))
+    stream = lambda i: SimpleNamespace(cuda_stream=0, device=torch.device("cuda", i))  # noqa: E731
+    with pytest.raises(ValueError, match="another device"):
+        mm.make_opts(grad_scale=scale, stream=stream(0))
+    assert mm.make_opts(grad_scale=scale, stream=stream(1))[0].grad_scale == P
