@@ -52,6 +52,14 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 }
+// barrier() waits for no memory access.  LDS stores that other waves read
+// behind one are followed by lds_release(), those reads led by lds_acquire().
+__device__ __forceinline__ void lds_release() { __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local"); }
+__device__ __forceinline__ void lds_acquire() { __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local"); }
+__device__ __forceinline__ void wave_fence() {  // orders a wave's LDS accesses, which execute in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // Chunk c (16 bytes) of a k-contiguous LDS row r sits at c ^ swz(r): any 16
 // consecutive rows of one chunk are spread over all banks.
@@ -420,6 +428,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
           if (have) a.tlogit[ci] = l;
         }
       }
+      lds_release();  // join() reads what other waves put into st
     } else {
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
@@ -469,6 +478,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
             const int r = lane & 31, c = 4 * i + 2 * pq + hi;
             *reinterpret_cast<u32x4_t*>(own + r * 128 + ((c ^ (r & 7)) * 16)) = pk;
           }
+        wave_fence();
         uint16_t* const block = a.prob + (tok0 + wn * WN + j * 32) * p.cols + (vw - p.v0);
         u32x4_t line[4];
 #pragma unroll
@@ -476,6 +486,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
           const int r = 8 * q + (lane >> 3), c = lane & 7;
           line[q] = *reinterpret_cast<const u32x4_t*>(own + r * 128 + ((c ^ (r & 7)) * 16));
         }
+        wave_fence();  // before the next 32 tokens' values
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = 8 * q + (lane >> 3), c = lane & 7;
@@ -488,6 +499,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   // token a thread of waves 4-7.
   auto join = [&](int64_t tok0, int64_t v0) {
     if constexpr (STATS) {
+      lds_acquire();
       const int t = tid & (kXTile - 1);
       float m = st[t].x;
 #pragma unroll
@@ -1030,11 +1042,6 @@ __global__ __launch_bounds__(256) void k_xent_dx(const XentArgs a, int splits) {
 // layout (32 rows an instruction), the depth split over four waves: 32 tokens 34
 // us a call against 25, at 151936 x 2048 234 against 140.
 // A token stands in its own column, so what an uncounted one holds stays there.
-__device__ __forceinline__ void wave_fence() {  // orders a wave's LDS accesses, which execute in order
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 template <int NT>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2))) void k_xent_few(const XentArgs a,
                                                                                          int blocks) {
