@@ -51,3 +51,37 @@ def test_pieces_of_a_large_call():
     mag = (soft.abs() * ok[:, None] * c).t() @ clean.double().abs()
     tol = tol_dw + len(t) * (copies - 1) * ULP32 * mag
     assert bool(((gw.double().cpu() - dw).abs() <= tol + RB * (dw.abs() + tol)).all())
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_loss_of_few_tokens_over_many_rounds(n):
+    """Every workgroup's largest logit stands in its first round of words, and
+    64 rounds follow that do not change the maximum: its weight stays 1.
+
+    x has one entry (1, 1/2, 1/4 or -1) and w one column (29.0 or 0), so the logits
+    are exact in fp32.  What the arithmetic may lose: the exponent's argument is
+    the difference of two fp32 values of log2(e) times at most 29.0, below 64,
+    each rounded by at most 2^-19 (a relative 2^-19 ln 2 of the sum; allowed
+    three times: in a lane, between lanes, between workgroups); 2^-24 for each of
+    the additions that a term goes through (32 words of a tile, 64 rounds, two
+    lanes, 32 workgroups of a lane) and 2^-22 for v_exp_f32, together below 64 *
+    2^-22; and log, the sum with the maximum and the difference with the target's
+    logit, each half a unit of a value below 64, 2^-19."""
+    print(f"[case] xent rounds {n}", flush=True)
+    rows, first = 1 << 23, 2048 * 64
+    w = torch.zeros(rows, 8, dtype=BF16)
+    w[:first:4, 0] = 29.0
+    x = torch.zeros(n, 8, dtype=BF16)
+    x[:, 0] = torch.tensor([1.0, 0.5, 0.25, -1.0])[torch.arange(n) % 4]
+    t = torch.tensor([0, 1, rows - 1])[torch.arange(n) % 3]
+    high, low = first // 4, rows - first // 4
+    lx = x[:, 0].double() * 29.0
+    top = lx.clamp(min=0.0)
+    lse = top + (high * (lx - top).exp() + low * (-top).exp()).log()
+    want = lse - x[:, 0].double() * w[t, 0].double()
+    got, tok, _, _ = mm.cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV), grad=False)
+    tol = 6 * 2.0 ** -19 + 64 * 2.0 ** -22
+    err = (tok.double().cpu() - want).abs()
+    print(f"  off by at most {float(err.max()):.2e} of {tol:.2e}", flush=True)
+    assert bool((err <= tol).all())
+    assert abs(float(got) - float(want.mean())) <= tol + ULP32 * float(want.mean())
