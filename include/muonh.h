@@ -175,6 +175,9 @@ typedef struct muonh_opts {
                                    are identical for every value. */
   int          hyperball_step;  /* MUONH_HB_STEP_UNIT (default) or MUONH_HB_STEP_RADIUS; also
                                    used by frob_project */
+  uint32_t     opts_bytes;      /* sizeof(muonh_opts) as the caller was compiled, set by
+                                   muonh_default_opts; 0: a caller of the structure that ended
+                                   with `deterministic`, and no field behind it is read */
   const int*   tile_sizes;      /* host, n entries, read during the call: per-matrix tile side
                                    for muonh_step / ns_orthogonalize (0: full-matrix NS; else
                                    the tile_T rules), overriding tile_T -- per-layer tile
@@ -190,8 +193,17 @@ typedef struct muonh_opts {
                                    NULL (default): G itself.  Not used by the other entry points */
 } muonh_opts;
 
-/* Fill *o with the defaults listed above. */
+/* Fill *o with the defaults listed above.  muonh_default_opts(&o) passes the
+ * size of the structure that the caller is compiled with on to
+ * muonh_default_opts_sized, which writes that many bytes and no more; fields that
+ * are added later are so never written to, nor read from, a caller that does not
+ * have them.  The function of the former name (called as (muonh_default_opts)(&o)
+ * or from programs compiled without the size) fills the structure up to
+ * `deterministic` and leaves opts_bytes 0: such a program's steps use G itself.
+ * Other languages call muonh_default_opts_sized. */
 void muonh_default_opts(muonh_opts* o);
+void muonh_default_opts_sized(muonh_opts* o, size_t bytes);
+#define muonh_default_opts(o) muonh_default_opts_sized((o), sizeof(muonh_opts))
 
 /*
  * muonh_step -- one full optimizer step (momentum -> NS -> hook) for n matrices.

@@ -39,7 +39,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char, c_double, c_float, c_int, c_int64, c_size_t, c_uint64, c_void_p
+from ctypes import POINTER, c_char, c_double, c_float, c_int, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuonh.so")
 
@@ -52,7 +52,7 @@ MUONH_HB_STEP_UNIT, MUONH_HB_STEP_RADIUS = 0, 1
 MUONH_REDUCE_MEAN, MUONH_REDUCE_SUM = 0, 1
 
 EXPORTED = (
-    "muonh_default_opts", "muonh_step", "muonh_step_noalloc", "adamh_step", "ns_orthogonalize", "frob_project", "muonh_get_flags",
+    "muonh_default_opts", "muonh_default_opts_sized", "muonh_step", "muonh_step_noalloc", "adamh_step", "ns_orthogonalize", "frob_project", "muonh_get_flags",
     "muonh_reset_flags", "muonh_strerror", "muonh_release", "muonh_plan_query",
     "muonh_profile_begin", "muonh_profile_read", "muonh_version", "muonh_last_error",
     "muonh_grad_norm_workspace", "muonh_grad_norm", "muonh_clip_grads",
@@ -93,6 +93,7 @@ class Opts(ctypes.Structure):
         ("weight_decay", c_float),
         ("lanes", c_int),
         ("hyperball_step", c_int),
+        ("opts_bytes", c_uint32),
         ("tile_sizes", POINTER(c_int)),
         ("param_dtype", c_int),
         ("deterministic", c_int),
@@ -135,6 +136,8 @@ def load(path: str = LIB_PATH):
     pp = POINTER(c_void_p)
     lib.muonh_default_opts.argtypes = [POINTER(Opts)]
     lib.muonh_default_opts.restype = None
+    lib.muonh_default_opts_sized.argtypes = [POINTER(Opts), c_size_t]
+    lib.muonh_default_opts_sized.restype = None
     lib.muonh_step.argtypes = [pp, pp, pp, POINTER(c_int64), c_int, c_float, c_float, c_int,
                                POINTER(c_float), c_int, POINTER(Opts)]
     lib.muonh_step.restype = c_int
@@ -240,7 +243,7 @@ def make_opts(state_dtype=MUONH_BF16, ns_dtype="bf16", ns_precision="h16", coeff
     buffers the struct points to."""
     lib = load()
     o = Opts()
-    lib.muonh_default_opts(ctypes.byref(o))
+    lib.muonh_default_opts_sized(ctypes.byref(o), ctypes.sizeof(o))
     o.state_dtype = state_dtype
     o.ns_dtype = {"bf16": MUONH_BF16, "f32": MUONH_F32}[ns_dtype]
     o.ns_precision = _NS_PRECISION[ns_precision]

@@ -6,6 +6,7 @@
 //   k_hook_reduce, k_hook_write          (Hyperball or RadialBrake)
 // all queued on the caller's stream with no host synchronization.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -224,6 +225,11 @@ int ensure_ws(State& st, int64_t bytes) {
 
 bool finite_f(float v) { return std::isfinite(v); }
 
+// The options before the first field that was added behind them: all that a
+// caller has whose opts_bytes does not name the whole structure.
+constexpr size_t kShortOpts = offsetof(muonh_opts, grad_scale);
+static_assert(kShortOpts == 104 && sizeof(muonh_opts) == 112, "fields of muonh_opts keep their places");
+
 struct Resolved {
   muonh_opts o;
   float coeffs[3 * kMaxK];
@@ -231,7 +237,7 @@ struct Resolved {
 
 int resolve(const muonh_opts* in, int K, Resolved& r) {
   muonh_default_opts(&r.o);
-  if (in) r.o = *in;
+  if (in) memcpy(&r.o, in, in->opts_bytes == sizeof(muonh_opts) ? sizeof(muonh_opts) : kShortOpts);
   const muonh_opts& o = r.o;
   if (o.param_dtype != MUONH_F32) return MUONH_EINVAL;  // fp32 master weights only
   if (o.deterministic != 0 && o.deterministic != 1) return MUONH_EINVAL;
@@ -927,31 +933,38 @@ using namespace muonh;
 
 extern "C" {
 
-void muonh_default_opts(muonh_opts* o) {
+void muonh_default_opts_sized(muonh_opts* o, size_t bytes) {
   if (!o) return;
-  memset(o, 0, sizeof(*o));
-  o->stream = nullptr;
-  o->state_dtype = MUONH_BF16;
-  o->ns_dtype = MUONH_BF16;
-  o->ns_precision = MUONH_NS_H16;
-  o->coeffs = nullptr;
-  o->ns_eps = 1e-7f;
-  o->zero_rel_eps = 1e-6f;
-  o->hook = MUONH_HOOK_HYPERBALL;
-  o->outward = 0.5f;
-  o->inward = 1.0f;
-  o->rb_eps = 1e-15f;
-  o->workspace_limit = 0;
-  o->momentum_ema = 0;
-  o->nesterov = 0;
-  o->weight_decay = 0.f;
-  o->lanes = 0;
-  o->hyperball_step = MUONH_HB_STEP_UNIT;
-  o->tile_sizes = nullptr;
-  o->param_dtype = MUONH_F32;
-  o->deterministic = 1;
-  o->grad_scale = nullptr;
+  muonh_opts d;
+  memset(&d, 0, sizeof(d));
+  d.stream = nullptr;
+  d.state_dtype = MUONH_BF16;
+  d.ns_dtype = MUONH_BF16;
+  d.ns_precision = MUONH_NS_H16;
+  d.coeffs = nullptr;
+  d.ns_eps = 1e-7f;
+  d.zero_rel_eps = 1e-6f;
+  d.hook = MUONH_HOOK_HYPERBALL;
+  d.outward = 0.5f;
+  d.inward = 1.0f;
+  d.rb_eps = 1e-15f;
+  d.workspace_limit = 0;
+  d.momentum_ema = 0;
+  d.nesterov = 0;
+  d.weight_decay = 0.f;
+  d.lanes = 0;
+  d.hyperball_step = MUONH_HB_STEP_UNIT;
+  d.opts_bytes = bytes >= sizeof(d) ? (uint32_t)sizeof(d) : 0u;
+  d.tile_sizes = nullptr;
+  d.param_dtype = MUONH_F32;
+  d.deterministic = 1;
+  d.grad_scale = nullptr;
+  memcpy(o, &d, std::min(bytes, sizeof(d)));
+  // what a newer caller has and this library does not know
+  if (bytes > sizeof(d)) memset(reinterpret_cast<char*>(o) + sizeof(d), 0, bytes - sizeof(d));
 }
+
+void (muonh_default_opts)(muonh_opts* o) { muonh_default_opts_sized(o, kShortOpts); }
 
 int muonh_step(void* const params[], const void* const grads[], void* const moms[], const int64_t shapes[],
                int n, float eta, float beta, int K, const float rho[], int tile_T, const muonh_opts* opts) {
@@ -1212,7 +1225,7 @@ int muonh_profile_read(muonh_kernel_stat* out, int max, int* n_out) {
   return rc;
 }
 
-const char* muonh_version(void) { return "libmuonh 0.1 (gfx950)"; }
+const char* muonh_version(void) { return "libmuonh 0.2 (gfx950)"; }
 
 const char* muonh_last_error(void) { return g_last_error; }
 
