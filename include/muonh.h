@@ -340,7 +340,8 @@ int frob_project(void* const W[], const void* const U[], const int64_t shapes[],
  * independent as long as their buffers are, nothing is allocated, and every
  * call can be captured into a graph, also as the first one.  `stream` is a
  * hipStream_t of the current device (NULL: the null stream) and no call waits
- * for the device.  Arguments are validated before any work is queued
+ * for the device, nor for a call on another thread (but while
+ * muonh_profile_begin is in effect).  Arguments are validated before any work is queued
  * (MUONH_EINVAL; MUONH_ENOMEM: the workspace is too small).  All sums have a
  * fixed order: results are bitwise reproducible.
  * ---------------------------------------------------------------------------

@@ -11,6 +11,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <list>
 #include <mutex>
@@ -141,7 +142,7 @@ struct State {
   std::list<CachedPlan> plans;  // most recent first
   hipStream_t side[kMaxLanes] = {};  // lanes 1.. (created on first use; [0] unused)
   hipEvent_t ev_gate[kMaxLanes] = {}, ev_join[kMaxLanes] = {};
-  bool profiling = false;
+  std::atomic<bool> profiling{false};  // read outside the lock by the calls that share nothing else
   std::vector<ProfRec> prof;
 };
 
@@ -907,9 +908,7 @@ int validate_common(const int64_t* shapes, int n, int K, int tile_T) {
 
 ProfScope::ProfScope(hipStream_t s, int cls, double flops, double bytes)
     : s_(s), cls_(cls), flops_(flops), bytes_(bytes) {
-  State& st = S();
-  std::lock_guard<std::mutex> lk(st.mu);
-  if (!st.profiling) return;
+  if (!S().profiling.load(std::memory_order_relaxed)) return;
   if (hipEventCreate(&e0_) != hipSuccess) e0_ = nullptr;
   if (e0_) (void)hipEventRecord(e0_, s_);
 }

@@ -22,8 +22,9 @@ int hip_fail(hipError_t e, const char* what);
   } while (0)
 
 // Event pair around the launches of its scope while muonh_profile_begin is in
-// effect; nothing otherwise.  Takes the library's lock: for entry points that
-// do not hold it.
+// effect; nothing otherwise.  Takes the library's lock to hand in a finished
+// pair: for entry points that do not hold it, which wait for nobody while
+// nothing is profiled (a call that holds the lock may wait for the device).
 class ProfScope {
  public:
   ProfScope(hipStream_t s, int cls, double flops, double bytes);
