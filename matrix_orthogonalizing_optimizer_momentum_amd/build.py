@@ -5,7 +5,8 @@
 compiles every csrc/*.hip with hipcc --offload-arch=gfx950, the host-only
 planner with g++, and links them into libmuonh.so next to this file; beside it
 _tensors.so, the Python extension that reads lists of torch tensors
-(binding/tensors.cpp, host code only).
+(binding/tensors.cpp, host code only).  libmuonh.so needs hipcc and g++ alone;
+the extension, torch with its headers.
 """
 from __future__ import annotations
 
@@ -81,16 +82,30 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
         cmds.append(["g++", *HOST_FLAGS, "-c", src, "-o", obj])
         objs.append(obj)
-    cmds.append(binding_cmd(BINDING_OUT + ".tmp"))
-    jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 4)))
+    # The library needs no torch: it is linked whatever becomes of the extension.
+    try:
+        binding = binding_cmd(BINDING_OUT + ".tmp")
+    except ImportError as e:
+        binding = None
+        print(f"without {os.path.basename(BINDING_OUT)} (lists of torch tensors): {e}", file=sys.stderr)
+    jobs = jobs or min(len(cmds) + 1, max(1, (os.cpu_count() or 4)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        for out in ex.map(_run, cmds):
+        done = [ex.submit(_run, cmd) for cmd in cmds]
+        extension = ex.submit(_run, binding) if binding else None
+        for f in done:
+            out = f.result()
             if verbose and out.strip():
                 print(out)
     tmp = OUT + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, OUT)
-    os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
+    if os.path.exists(BINDING_OUT):
+        os.remove(BINDING_OUT)  # of other sources, until it is replaced
+    if extension:
+        out = extension.result()
+        if verbose and out.strip():
+            print(out)
+        os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
     return OUT
 
 
