@@ -370,7 +370,8 @@ int muonh_grad_norm(const void* const grads[], const int64_t numel[], const int 
  * muonh_clip_grads -- muonh_grad_norm, then outs[t] = coef * grads[t] in the
  * gradient's own dtype (one rounding).  outs[t] may be grads[t] (in place;
  * nothing is written when coef is 1); outs that overlap each other or another
- * gradient are refused (MUONH_EINVAL).  Workspace: muonh_grad_norm_workspace(n).
+ * gradient, and a total or coef that overlaps any of them or the other, are
+ * refused (MUONH_EINVAL).  Workspace: muonh_grad_norm_workspace(n).
  */
 int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_t numel[], const int dtypes[], int n,
                      float max_norm, float* total, float* coef, void* workspace, size_t workspace_bytes,
@@ -384,7 +385,8 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
  *   out     device, n x width, MUONH_F32 or MUONH_BF16 (one rounding)
  *   rows    1 .. 2^31 - 2;  n  0 .. 2^26, width  1 .. 2^18, together up to 2^36
  *           values of out (more: MUONH_ENOTIMPL);  scale  finite
- * Buffers need no more than their elements' alignment.
+ * Buffers need no more than their elements' alignment; out must not overlap
+ * table or ids (MUONH_EINVAL).
  */
 int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t width, const void* ids, int id_bits,
                     int64_t n, float scale, void* out, int out_dtype, void* stream);
@@ -398,7 +400,8 @@ int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t wi
  * gradient of a tied table.  The tokens are sorted by id in the call, so each
  * row is a sum in a fixed order.
  *   dout    device, n x width, MUONH_F32 or MUONH_BF16
- *   dtable  device, rows x width, MUONH_F32 or MUONH_BF16, must not overlap dout
+ *   dtable  device, rows x width, MUONH_F32 or MUONH_BF16, must not overlap dout or
+ *           ids (MUONH_EINVAL)
  * Other arguments as muonh_embedding; n = 0 clears dtable (or leaves it).
  */
 size_t muonh_embedding_grad_workspace(int64_t n, int64_t rows, int64_t width);
@@ -426,7 +429,8 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
  *   dx          device, n x width, bf16, or NULL (not computed)
  *   dw          device, rows x width of dw_dtype (MUONH_BF16 / MUONH_F32), or
  *               NULL; accumulate = 1 adds to it (gradient accumulation)
- * No output may overlap w, targets or another output (dx may be x).
+ * No output may overlap w, targets or another output, nor token_loss x
+ * (MUONH_EINVAL); x is copied before the others are written (dx may be x).
  * Products take bf16 operands and sum in fp32.  The gradients see P rounded to
  * bf16 (at most 2^-8 of each value off), also where dw is fp32.
  * The vocabulary is taken in pieces for the gradients; the workspace decides

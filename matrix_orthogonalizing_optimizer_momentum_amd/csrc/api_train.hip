@@ -21,6 +21,13 @@ namespace {
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const void* p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p ? (uintptr_t)bytes : 0)}; }
+// Empty spans (a null pointer, no bytes) overlap nothing.
+bool overlap(const Span& x, const Span& y) { return x.lo < x.hi && y.lo < y.hi && x.lo < y.hi && y.lo < x.hi; }
+
 // ------------------------------------------------------------ gradient norm
 // Blocks of all tensors together: about 8 for each of the 256 CUs (all
 // resident at once), at least kMinChunk bytes each.
@@ -58,14 +65,9 @@ int check_grads(const void* const* grads, const int64_t* numel, const int* dtype
 // Clipping writes outs[i] while it reads grads: outs must not overlap each
 // other, nor a gradient other than their own, in place.
 int check_outs(const void* const* grads, void* const* outs, const int64_t* numel, const int* dtypes, int n) {
-  struct Span {
-    uintptr_t lo, hi;
-  };
   std::unique_ptr<Span[]> v(new (std::nothrow) Span[n]);
   if (!v) return MUONH_ENOMEM;
-  auto span = [&](const void* p, int i) {
-    return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)grad_bytes(numel[i], dtypes[i])};
-  };
+  auto span = [&](const void* p, int i) { return span_of(p, grad_bytes(numel[i], dtypes[i])); };
   int m = 0;
   for (int i = 0; i < n; ++i)
     if (numel[i] > 0) v[m++] = span(outs[i], i);
@@ -79,6 +81,20 @@ int check_outs(const void* const* grads, void* const* outs, const int64_t* numel
     const Span* const o = std::partition_point(v.get(), end, [&](const Span& x) { return x.hi <= g.lo; });
     if (o != end && o->lo < g.hi) return MUONH_EINVAL;
   }
+  return MUONH_OK;
+}
+
+// Its scalars are written before the gradients are read again, and read beside
+// the writing of outs.
+int check_clip_scalars(const float* total, const float* coef, const void* const* grads, void* const* outs,
+                       const int64_t* numel, const int* dtypes, int n) {
+  const Span t = span_of(total, 4), c = span_of(coef, 4);
+  if (overlap(t, c)) return MUONH_EINVAL;
+  for (int i = 0; i < n; ++i)
+    for (const void* p : {grads[i], (const void*)outs[i]}) {
+      const Span s = span_of(p, grad_bytes(numel[i], dtypes[i]));
+      if (overlap(s, t) || overlap(s, c)) return MUONH_EINVAL;
+    }
   return MUONH_OK;
 }
 
@@ -346,6 +362,8 @@ int muonh_clip_grads(const void* const grads[], void* const outs[], const int64_
   const int rd = check_outs(grads, outs, numel, dtypes, n);
   if (rd != MUONH_OK) return rd;
   if (workspace_bytes < muonh_grad_norm_workspace(n)) return MUONH_ENOMEM;
+  const int rs = check_clip_scalars(total, coef, grads, outs, numel, dtypes, n);
+  if (rs != MUONH_OK) return rs;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int rq = queue_norm(grads, numel, dtypes, n, bytes, false, max_norm, total, coef, nullptr, workspace, s);
   if (rq != MUONH_OK) return rq;
@@ -368,6 +386,9 @@ int muonh_embedding(const void* table, int table_dtype, int64_t rows, int64_t wi
   if (!table || misaligned(table, dtype_size(table_dtype))) return MUONH_EINVAL;
   if (n > 0 && (!out || misaligned(out, dtype_size(out_dtype)))) return MUONH_EINVAL;
   if (n == 0) return MUONH_OK;
+  const Span o = span_of(out, n * width * dtype_size(out_dtype));
+  if (overlap(o, span_of(table, rows * width * dtype_size(table_dtype))) || overlap(o, span_of(ids, n * (id_bits / 8))))
+    return MUONH_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   ProfScope pf(s, PC_EMB, 0, (double)n * (double)width * (double)(dtype_size(table_dtype) + dtype_size(out_dtype)));
   const EmbedArgs a{table, ids, out, n, rows, width, scale, id_bits,
@@ -394,6 +415,9 @@ int muonh_embedding_grad(const void* ids, int id_bits, int64_t n, const void* do
   if (!workspace || misaligned(workspace, 256)) return MUONH_EINVAL;
   const EmbedPlan p = embed_plan(n, rows, width);
   if (workspace_bytes < (size_t)p.bytes) return MUONH_ENOMEM;
+  const Span o = span_of(dtable, rows * width * dtype_size(dtable_dtype));
+  if (overlap(o, span_of(dout, n * width * dtype_size(dout_dtype))) || overlap(o, span_of(ids, n * (id_bits / 8))))
+    return MUONH_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* const ws = reinterpret_cast<char*>(workspace);
   auto u32 = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
@@ -473,6 +497,15 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
   rc = xent_plan(w, n, rows, width, dx != nullptr, dw != nullptr,
                  (int64_t)std::min<size_t>(workspace_bytes, (size_t)INT64_MAX), p);
   if (rc != MUONH_OK) return rc;
+  // x is copied before anything but token_loss is written
+  const Span outs[] = {span_of(loss, 4), span_of(token_loss, 4 * n), span_of(dx, 2 * n * width),
+                       span_of(dw, rows * width * dtype_size(dw_dtype))};
+  for (const Span& o : outs) {
+    if (overlap(o, span_of(w, 2 * rows * width)) || overlap(o, span_of(targets, n * (id_bits / 8)))) return MUONH_EINVAL;
+    for (const Span* other = outs; other != &o; ++other)
+      if (overlap(*other, o)) return MUONH_EINVAL;
+  }
+  if (overlap(outs[1], span_of(x, 2 * n * width))) return MUONH_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* const ws = reinterpret_cast<char*>(workspace);
   auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };

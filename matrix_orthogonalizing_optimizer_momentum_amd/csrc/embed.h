@@ -15,7 +15,10 @@ constexpr int kSortThreads = 256;
 constexpr int kSortBits = 11;      // digit bits of one sort pass, at most
 constexpr int kSortMaxBlocks = 256;  // 2^20 tokens of 256 values: 220 us, with 64 blocks 312
 constexpr int kSoloThreads = 1024;  // the sort in one workgroup:
-constexpr int kSoloItems = 8;       // tokens per thread (8192 tokens on 50257 x 768: 37 us, by passes 52; 16384: 61 and 56)
+// Tokens per thread.  A gradient of 8192 tokens on 50257 x 768 bf16 to fp32: 37 us,
+// by passes 50 (into one buffer, which stays in the last-level cache; 47.6 and
+// 54.5 where calls take turns with two), of 16384 tokens 60 and 55.
+constexpr int kSoloItems = 8;
 constexpr int kSoloBits = 9;        // digit bits of one of its passes
 constexpr int64_t kSoloTokens = kSoloThreads * kSoloItems;
 constexpr int kRunMin = 8, kRunMax = 64;  // sorted tokens per piece of the gradient

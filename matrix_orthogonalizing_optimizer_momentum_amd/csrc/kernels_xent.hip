@@ -16,6 +16,11 @@
 // matrix cores) for one piece, and two products that read that P:
 // dx += P w_piece (fp32 across pieces) and dw_piece = P^T x.
 //
+// P's rounding is the one place below 32 bits.  8192 tokens, 50257 x 768: bf16
+// results are 0.00168 of their norm from 64 bits, 0.00166 with P in fp32; an fp32
+// dw is 2.6e-4 from the one with P in fp32.  A second bf16 part of P for what the
+// first leaves would double the two products that read it, half of the call.
+//
 // All products run on one 256 x 256 main loop of 8 waves, D[m][n] =
 // sum_k A[m][k] B[n][k]: v_mfma_f32_32x32x16_bf16, 64-deep operand stages
 // double buffered in LDS, brought in by direct global -> LDS loads; the two

@@ -223,7 +223,9 @@ def cross_entropy(x, w, targets, reduction="mean", grad=True, grad_scale=1.0, ig
     in float32, and the gradients times ``grad_scale`` (``None`` with
     ``grad=False``).  ``grad`` may also be "x" or "w" for one of the two.
     ``dx`` (bfloat16) and ``dw`` (bfloat16 or float32, ``dw_dtype``) are
-    allocated unless given; ``accumulate`` adds to the given ``dw``.
+    allocated unless given; ``accumulate`` adds to the given ``dw``.  Both are
+    products of the softmax rounded to bfloat16 (2^-8 of each weight), summed in
+    float32: a float32 ``dw`` saves the rounding of its sums, not that one.
     ``workspace_limit`` (bytes) bounds the scratch memory: the vocabulary is
     taken in pieces that fit it.
     """
