@@ -85,7 +85,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     # The library needs no torch: it is linked whatever becomes of the extension.
     try:
         binding = binding_cmd(BINDING_OUT + ".tmp")
-    except ImportError as e:
+    except (ImportError, OSError) as e:  # OSError: a torch whose libraries do not load
         binding = None
         print(f"without {os.path.basename(BINDING_OUT)} (lists of torch tensors): {e}", file=sys.stderr)
     jobs = jobs or min(len(cmds) + 1, max(1, (os.cpu_count() or 4)))

@@ -33,9 +33,10 @@ def test_both_are_built(dry):
     assert any(b.BINDING in c for c in dry)
 
 
-def test_the_library_needs_no_torch(dry, monkeypatch, capsys):
+@pytest.mark.parametrize("error", [ImportError("No module named 'torch'"), OSError("libtorch_cpu.so: cannot open")])
+def test_the_library_needs_no_torch(dry, monkeypatch, capsys, error):
     def none(out):
-        raise ImportError("No module named 'torch'")
+        raise error
 
     monkeypatch.setattr(b, "binding_cmd", none)
     with open(b.BINDING_OUT, "w") as f:
