@@ -9,6 +9,7 @@
 #include <memory>
 #include <new>
 
+#include "checks.h"
 #include "desc.h"
 #include "embed.h"
 #include "grad.h"
@@ -18,15 +19,6 @@
 
 namespace muonh {
 namespace {
-
-int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span_of(const void* p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p ? (uintptr_t)bytes : 0)}; }
-// Empty spans (a null pointer, no bytes) overlap nothing.
-bool overlap(const Span& x, const Span& y) { return x.lo < x.hi && y.lo < y.hi && x.lo < y.hi && y.lo < x.hi; }
 
 // ------------------------------------------------------------ gradient norm
 // Blocks of all tensors together: about 8 for each of the 256 CUs (all
@@ -135,11 +127,6 @@ int queue_norm(const void* const* grads, const int64_t* numel, const int* dtypes
 }
 
 // ------------------------------------------------------------------ embedding
-bool bad_dtype(int d) { return d != MUONH_F32 && d != MUONH_BF16; }
-int64_t dtype_size(int d) { return d == MUONH_F32 ? 4 : 2; }
-int internal_dtype(int d) { return d == MUONH_F32 ? DT_F32 : DT_BF16; }
-bool misaligned(const void* p, int64_t a) { return (uintptr_t)p % a != 0; }
-
 // n tokens, a table of rows x width; n = 0 is allowed.
 int check_embedding(const void* ids, int id_bits, int64_t n, int64_t rows, int64_t width) {
   if (n < 0 || rows < 1 || rows >= INT32_MAX || width < 1) return MUONH_EINVAL;

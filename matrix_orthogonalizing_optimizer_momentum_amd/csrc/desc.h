@@ -168,4 +168,9 @@ struct Flags {
   unsigned long long nonfinite;
 };
 
+// The products around the optimizer step (product.h).
+constexpr int kXTile = 256;  // output tile side
+constexpr int kXStage = 64;  // depth of one operand stage
+constexpr int kXCus = 256;   // compute units, a multiple of the 8 XCDs
+
 }  // namespace muonh
