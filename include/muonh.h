@@ -449,6 +449,102 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
                         size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Between the embedding and the output layer.  The same rules as around the
+ * step: no state, scratch memory from the caller, validation before any work,
+ * sums in a fixed order.
+ *
+ * Activations in 8 bits, as written and read below: `q` holds one e4m3 byte (OCP
+ * FP8: 4 significant bits, largest 448, NaN but no infinity) for each value of
+ * an n x width matrix, `scales` one byte for each block of 32 values along a
+ * row, n x ceil(width / 32) (the last block of a row may be short): the
+ * biased exponent of a power of two (OCP E8M0; 255 is NaN).  A value is
+ * q 2^(scale - 127).  The scales written here are the least with no finite value
+ * of the block above 448 of it, and 10 (2^-117) at least: rounding to nearest
+ * even, a value is at most 2^-4 of itself off (2^-10 of the scale where it
+ * is below 2^-6 of it), and what is read back is exact in bf16 (from
+ * 1.9375 2^127 on it is 2^128, infinity).  An infinity or NaN is
+ * kept as NaN and reaches no other value.  Neither buffer needs alignment.
+ * ---------------------------------------------------------------------------
+ *
+ * muonh_rms_norm -- root-mean-square norm of the rows of x, or of the residual
+ * stream that x is added to:
+ *   h  = round(x + residual)   (to h's type; h = x without a residual)
+ *   rstd = (mean_j h_j^2 + eps)^-1/2,  xn = rstd h,  y = gain xn
+ *   x         device, n x width, MUONH_F32 or MUONH_BF16
+ *   residual  device, n x width of h_dtype, with h, or both NULL
+ *   gain      device, width floats, or NULL (1)
+ *   eps       finite, > 0
+ *   h         device, n x width of h_dtype; may be residual
+ *   y         device, n x width of y_dtype, or NULL
+ *   rstd      device, n floats, or NULL
+ *   q, scales device, a matrix in 8 bits, or both NULL: xn
+ *             (MUONH_PACK_NORMALIZED; what muonh_rms_norm_grad and, with the gain,
+ *             muonh_weight_grad read) or y (MUONH_PACK_OUTPUT)
+ *   n         0 .. 2^26;  width  1 .. 16384 (MUONH_ENOTIMPL above)
+ * Squares are summed in fp64, the rest is fp32, each output rounded once.  Other
+ * overlaps of an output with an input or an output are refused (MUONH_EINVAL).
+ */
+enum { MUONH_PACK_NORMALIZED = 0, MUONH_PACK_OUTPUT = 1 };
+int muonh_rms_norm(const void* x, int x_dtype, const void* residual, int h_dtype, const float* gain, float eps, int64_t n,
+                   int64_t width, void* h, void* y, int y_dtype, float* rstd, void* q, void* scales, int packs,
+                   void* stream);
+
+/*
+ * muonh_rms_norm_grad -- the gradients of muonh_rms_norm's input and gain:
+ *   xn = rstd x, or what q and scales stand for
+ *   dx = dres + rstd (gain dy - xn mean_j(gain_j dy_j xn_j)),
+ *   dgain = sum over the rows of dy xn
+ * dx is the gradient of x and of residual alike; dres, the gradient that reaches h
+ * on the residual's path, is added to it.
+ *   dy        device, n x width, MUONH_F32 or MUONH_BF16
+ *   x         device, n x width of dx_dtype: the norm's input (h), or NULL
+ *   q, scales device, xn in 8 bits, instead of x
+ *   rstd      device, n floats, as muonh_rms_norm gave them
+ *   gain      device, width floats, or NULL (1)
+ *   dres      device, n x width of dx_dtype, or NULL
+ *   dx        device, n x width of dx_dtype; may be dres
+ *   dgain     device, width floats, or NULL; accumulate = 1 adds to it
+ *   workspace needed with dgain
+ * Sums are fp32.  n = 0 clears dgain (or leaves it).
+ */
+size_t muonh_rms_norm_grad_workspace(int64_t n, int64_t width);
+int muonh_rms_norm_grad(const void* dy, int dy_dtype, const void* x, const void* q, const void* scales, const float* rstd,
+                        const float* gain, const void* dres, int dx_dtype, int64_t n, int64_t width, void* dx,
+                        float* dgain, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * muonh_mx_pack, muonh_mx_unpack -- a matrix to 8 bits, and back (rounded once to
+ * out_dtype).  x, out: MUONH_F32 or MUONH_BF16, n x width; n 0 .. 2^26, width
+ * 1 .. 2^20.
+ */
+int muonh_mx_pack(const void* x, int x_dtype, int64_t n, int64_t width, void* q, void* scales, void* stream);
+int muonh_mx_unpack(const void* q, const void* scales, int64_t n, int64_t width, void* out, int out_dtype, void* stream);
+
+/*
+ * muonh_weight_grad -- the gradient of a weight W of rows x width behind
+ * z_t = W (gain x_t), from its activations in 8 bits:
+ *   dw[o][i] = scale gain_i sum_t dz[t][o] x[t][i]
+ * With xn as x (MUONH_PACK_NORMALIZED) and the norm's gain this is the gradient
+ * of a weight that reads the norm's output.
+ *   dz        device, n x rows, bf16
+ *   q, scales device, n x width in 8 bits (products see them rounded to bf16:
+ *             exact for scales that this library writes)
+ *   gain      device, width floats, or NULL (1);  scale  finite
+ *   dw        device, rows x width of dw_dtype (MUONH_F32 / MUONH_BF16);
+ *             accumulate = 1 adds to it; must not overlap the inputs
+ *   n         0 .. 2^22;  rows, width  1 .. 2^20, together up to 2^37 values of dw
+ *             and 2^35 of dz or x (MUONH_ENOTIMPL above); n = 0 clears dw (or leaves it)
+ * Sums are fp32, rounded once.  Rows of dz that are not a multiple of 8 values, or
+ * not on a 16-byte grid, are copied to the workspace once; of dz only its address
+ * matters to muonh_weight_grad_workspace.
+ */
+size_t muonh_weight_grad_workspace(const void* dz, int64_t n, int64_t rows, int64_t width);
+int muonh_weight_grad(const void* dz, const void* q, const void* scales, const float* gain, float scale, int64_t n,
+                      int64_t rows, int64_t width, void* dw, int dw_dtype, int accumulate, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * Device flag counters, accumulated since the last reset:
  *   out[0] matrices whose orthogonalized update had zero norm,
  *   out[1] Hyperball radius restores (numerically zero post-update weight),

@@ -34,6 +34,13 @@ Around the step (``gradients.py``):
   ``embedding_grad(ids, dout, rows, scale=1.0, out=None, out_dtype=None, accumulate=False)``
 * ``cross_entropy(x, w, targets, reduction="mean", grad=True, ...)``: the output
   layer's loss with its gradients
+
+Between the embedding and the output layer (``activations.py``):
+
+* ``rms_norm(x, gain=None, residual=None, eps=1e-6, pack=None, ...)``,
+  ``rms_norm_grad(dy, x, rstd, gain=None, dres=None, ...)``
+* ``mx_pack(x)``, ``mx_unpack(packed, out_dtype=torch.bfloat16)``: activations in 8 bits
+* ``weight_grad(dz, packed, gain=None, scale=1.0, ...)``: a weight's gradient from them
 """
 from __future__ import annotations
 
@@ -50,6 +57,7 @@ _NS_PRECISION = {"fold": MUONH_NS_FOLD, "x32": MUONH_NS_X32, "h16": MUONH_NS_H16
 MUONH_HOOK_HYPERBALL, MUONH_HOOK_RADIAL_BRAKE, MUONH_HOOK_NONE, MUONH_HOOK_RELATIVE = 0, 1, 2, 3
 MUONH_HB_STEP_UNIT, MUONH_HB_STEP_RADIUS = 0, 1
 MUONH_REDUCE_MEAN, MUONH_REDUCE_SUM = 0, 1
+MUONH_PACK_NORMALIZED, MUONH_PACK_OUTPUT = 0, 1
 
 EXPORTED = (
     "muonh_default_opts", "muonh_default_opts_sized", "muonh_step", "muonh_step_noalloc", "adamh_step", "ns_orthogonalize", "frob_project", "muonh_get_flags",
@@ -58,6 +66,8 @@ EXPORTED = (
     "muonh_grad_norm_workspace", "muonh_grad_norm", "muonh_clip_grads",
     "muonh_embedding", "muonh_embedding_grad_workspace", "muonh_embedding_grad",
     "muonh_cross_entropy_workspace", "muonh_cross_entropy",
+    "muonh_rms_norm", "muonh_rms_norm_grad_workspace", "muonh_rms_norm_grad", "muonh_mx_pack", "muonh_mx_unpack",
+    "muonh_weight_grad_workspace", "muonh_weight_grad",
 )
 
 
@@ -191,6 +201,23 @@ def load(path: str = LIB_PATH):
                                         c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p,
                                         c_size_t, c_void_p]
     lib.muonh_cross_entropy.restype = c_int
+    lib.muonh_rms_norm.argtypes = [c_void_p, c_int, c_void_p, c_int, c_void_p, c_float, c_int64, c_int64, c_void_p,
+                                   c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p]
+    lib.muonh_rms_norm.restype = c_int
+    lib.muonh_rms_norm_grad_workspace.argtypes = [c_int64, c_int64]
+    lib.muonh_rms_norm_grad_workspace.restype = c_size_t
+    lib.muonh_rms_norm_grad.argtypes = [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                        c_int64, c_int64, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.muonh_rms_norm_grad.restype = c_int
+    lib.muonh_mx_pack.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p]
+    lib.muonh_mx_pack.restype = c_int
+    lib.muonh_mx_unpack.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int, c_void_p]
+    lib.muonh_mx_unpack.restype = c_int
+    lib.muonh_weight_grad_workspace.argtypes = [c_void_p, c_int64, c_int64, c_int64]
+    lib.muonh_weight_grad_workspace.restype = c_size_t
+    lib.muonh_weight_grad.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_int64, c_int64, c_int64, c_void_p,
+                                      c_int, c_int, c_void_p, c_size_t, c_void_p]
+    lib.muonh_weight_grad.restype = c_int
     _LIB = lib
     return lib
 
@@ -482,8 +509,11 @@ def profile_read():
 
 
 def __getattr__(name):
-    # gradients.py needs torch at import, which nothing above does
+    # gradients.py and activations.py need torch at import, which nothing above does
     if name in ("clip_grads", "cross_entropy", "embedding", "embedding_grad", "grad_norm"):
         from . import gradients
         return getattr(gradients, name)
+    if name in ("Normed", "Packed", "mx_pack", "mx_unpack", "rms_norm", "rms_norm_grad", "weight_grad"):
+        from . import activations
+        return getattr(activations, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

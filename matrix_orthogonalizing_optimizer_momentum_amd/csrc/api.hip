@@ -155,7 +155,8 @@ const char* kClassNames[] = {"momentum_prep", "ns_gram_G1", "ns_poly_G2",       
                              "hook_reduce",   "hook_write", "sumsq",            "finalize",
                              "ns_tile_resident", "adam_moments", "adam_write", "ns_tile_fused",
                              "grad_sumsq",    "grad_scale", "embedding",        "embedding_sort",
-                             "embedding_grad", "xent_prepare", "xent_logits",   "xent_prob", "xent_grad"};
+                             "embedding_grad", "xent_prepare", "xent_logits",   "xent_prob", "xent_grad",
+                             "rms_norm",      "rms_norm_grad", "mx_pack",         "wgrad_prepare", "wgrad"};
 static_assert(sizeof(kClassNames) / sizeof(kClassNames[0]) == PC_N, "one name per kernel class");
 
 // ------------------------------------------------------------------ helpers

@@ -1,0 +1,109 @@
+// Activations to 8 bits and back (gfx950); the format is mx.h's.
+//
+// One pass each at the rate of memory: a thread takes 8 values of a row, the 4
+// threads of a block of 32 find its largest magnitude by lane exchanges, and
+// the values leave as 8 bytes with one scale byte a block.  A row belongs to a power of two of
+// threads, so that short rows share a workgroup and nothing is divided; a
+// thread has kRows rows in flight.
+#include <algorithm>
+
+#include "act.h"
+#include "common.h"
+#include "mx.h"
+
+namespace muonh {
+
+namespace {
+
+constexpr int kRows = 4;
+
+// Threads of a row (their logarithm): whole blocks, at most the workgroup's 256.
+int row_log(int64_t width) {
+  int l = 2;
+  while (l < 8 && ((int64_t)8 << l) < width) ++l;
+  return l;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_mx_pack(const MxArgs a, int lg) {
+  const int64_t width = a.width, nblk = mx_blocks(width);
+  const T* const in = static_cast<const T*>(a.in);
+  const int64_t c = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+  const int m = (int)min<int64_t>(max<int64_t>(width - 8 * c, 0), 8);
+  const int64_t per = 256 >> lg, step = per * gridDim.x;
+  for (int64_t r0 = blockIdx.x * per + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * step) {
+    Raw8<T> raw[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (m == 8 && r0 + u * step < a.n) raw[u].load_any(in, (r0 + u * step) * width + 8 * c);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + u * step;
+      if (r >= a.n) break;  // the same for the 4 lanes of a block
+      float v[8];
+      if (m == 8) raw[u].unpack(v);
+      else load_first(in, r * width + 8 * c, m, v);
+      const uint32_t sc = mx_scale(quad_max(finite_max(v)));
+      const u32x2_t q = to_e4m3(v, mx_inverse(sc));
+      if (m == 8) store_q8(a.q + r * width + 8 * c, q);
+      else store_q8(a.q + r * width + 8 * c, q, m);
+      if (c % 4 == 0 && m > 0) gmem(a.scales)[r * nblk + c / 4] = (uint8_t)sc;
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_mx_unpack(const MxArgs a, int lg) {
+  const int64_t width = a.width, nblk = mx_blocks(width);
+  T* const out = static_cast<T*>(a.out);
+  const int64_t c = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+  const int m = (int)min<int64_t>(max<int64_t>(width - 8 * c, 0), 8);
+  if (m == 0) return;
+  const int64_t per = 256 >> lg, step = per * gridDim.x;
+  for (int64_t r0 = blockIdx.x * per + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * step) {
+    u32x2_t q[kRows];
+    uint32_t sc[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + u * step;
+      if (r < a.n) {
+        sc[u] = gmem(a.scales)[r * nblk + c / 4];
+        q[u] = m == 8 ? load_q8(a.q + r * width + 8 * c) : load_q8(a.q + r * width + 8 * c, m);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + u * step;
+      if (r >= a.n) break;
+      float v[8];
+      from_e4m3(q[u], mx_factor(sc[u]), v);
+      if (m == 8) store8_any(out, r * width + 8 * c, v);
+      else store_first(out, r * width + 8 * c, m, v);
+    }
+  }
+}
+
+// Workgroups side by side over a row, and over the rows.
+dim3 grid(const MxArgs& a, int lg) {
+  const int64_t across = (a.width + ((int64_t)8 << lg) - 1) / ((int64_t)8 << lg), per = 256 >> lg;
+  const int64_t down = std::min<int64_t>((a.n + per * kRows - 1) / (per * kRows), std::max<int64_t>(1, 65536 / across));
+  return dim3((uint32_t)down, (uint32_t)across);
+}
+
+}  // namespace
+
+hipError_t launch_mx_pack(int dt, const MxArgs& a, hipStream_t s) {
+  const int lg = row_log(a.width);
+  if (dt == DT_BF16) k_mx_pack<bf16_t><<<grid(a, lg), 256, 0, s>>>(a, lg);
+  else k_mx_pack<float><<<grid(a, lg), 256, 0, s>>>(a, lg);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_unpack(int dt, const MxArgs& a, hipStream_t s) {
+  const int lg = row_log(a.width);
+  if (dt == DT_BF16) k_mx_unpack<bf16_t><<<grid(a, lg), 256, 0, s>>>(a, lg);
+  else k_mx_unpack<float><<<grid(a, lg), 256, 0, s>>>(a, lg);
+  return hipGetLastError();
+}
+
+}  // namespace muonh

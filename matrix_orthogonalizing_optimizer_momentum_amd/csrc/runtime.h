@@ -9,7 +9,8 @@ namespace muonh {
 // Kernel classes of muonh_profile_read.
 enum {
   PC_MOM = 0, PC_G1, PC_G2, PC_G3, PC_HR, PC_HW, PC_SQ, PC_FIN, PC_TILE, PC_AM, PC_AW, PC_T256,
-  PC_GNORM, PC_GSCALE, PC_EMB, PC_EMBSORT, PC_EMBGRAD, PC_XPREP, PC_XLOGIT, PC_XPROB, PC_XGRAD, PC_N
+  PC_GNORM, PC_GSCALE, PC_EMB, PC_EMBSORT, PC_EMBGRAD, PC_XPREP, PC_XLOGIT, PC_XPROB, PC_XGRAD,
+  PC_NORM, PC_NORMGRAD, PC_MX, PC_WPREP, PC_WGRAD, PC_N
 };
 
 // Records e as this thread's last HIP failure and returns MUONH_EHIP.

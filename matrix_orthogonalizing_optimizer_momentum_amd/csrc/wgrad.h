@@ -1,0 +1,30 @@
+// Layout and launchers of the weight gradient from 8-bit activations, shared by
+// the kernels and the entry point.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "act.h"
+
+namespace muonh {
+
+constexpr int64_t kWgMaxTokens = (int64_t)1 << 22, kWgMaxSide = (int64_t)1 << 20, kWgMaxValues = (int64_t)1 << 37;
+
+struct WgradArgs {
+  const uint16_t* dz;                // n x rows
+  const uint8_t* q;                  // n x width e4m3
+  const uint8_t* scales;             // n x mx_blocks(width)
+  const float* gain;                 // width, or nullptr
+  void* dw;                          // rows x width
+  uint16_t* xt;                      // width up to a tile rows of ldxt: q's values in bf16 along the tokens
+  uint16_t* dzc;                     // dz's rows [dfull, n), padded with zeros to a whole stage, of lddz
+  float* part;                       // [splits][rows][ldp], with splits > 1
+  int64_t n, npad, rows, width, ldxt, lddz, dfull, ldp;
+  float scale;
+  int32_t dw_dt, accumulate, splits;
+};
+
+hipError_t launch_wgrad_prepare(const WgradArgs& a, hipStream_t s);
+hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s);
+
+}  // namespace muonh
