@@ -1,4 +1,5 @@
-// Python extension `_tensors`: reads lists of torch tensors.
+// Python extension `_tensors`: reads lists of torch tensors (below), and makes the
+// calls of activations.py (activations.cpp).
 //
 // A call over a model's gradients needs five attributes of every tensor; read
 // through Python they cost 0.33 us a tensor, which at a hundred small tensors
@@ -11,6 +12,7 @@
 
 #include <exception>
 
+#include "activations.h"
 #include "muonh.h"
 
 namespace {
@@ -82,7 +84,17 @@ PyObject* table(PyObject*, PyObject* args) {
   return out;
 }
 
+PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
+}
+
 PyMethodDef methods[] = {{"table", table, METH_VARARGS, "table(tensors, what) -> (pointers, sizes, dtypes, device)"},
+                         {"bind", muonh_bind, METH_VARARGS, "bind(addresses of the entry points)"},
+                         {"rms_norm", fast(muonh_py_rms_norm), METH_FASTCALL, nullptr},
+                         {"rms_norm_grad", fast(muonh_py_rms_norm_grad), METH_FASTCALL, nullptr},
+                         {"mx_pack", fast(muonh_py_mx_pack), METH_FASTCALL, nullptr},
+                         {"mx_unpack", fast(muonh_py_mx_unpack), METH_FASTCALL, nullptr},
+                         {"weight_grad", fast(muonh_py_weight_grad), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -4,8 +4,8 @@
 
 compiles every csrc/*.hip with hipcc --offload-arch=gfx950, the host-only
 planner with g++, and links them into libmuonh.so next to this file; beside it
-_tensors.so, the Python extension that reads lists of torch tensors
-(binding/tensors.cpp, host code only).  libmuonh.so needs hipcc and g++ alone;
+_tensors.so, the Python extension that reads lists of torch tensors and makes the
+calls of activations.py (binding/*.cpp, host code only).  libmuonh.so needs hipcc and g++ alone;
 the extension, torch with its headers.
 """
 from __future__ import annotations
@@ -23,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libmuonh.so")
 BINDING = os.path.join(HERE, "binding", "tensors.cpp")
+BINDING_CALLS = os.path.join(HERE, "binding", "activations.cpp")
 BINDING_OUT = os.path.join(HERE, "_tensors.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "muonh")
 
@@ -56,13 +57,13 @@ def sources():
 
 
 def binding_cmd(out):
-    """The g++ line of the tensor-list extension, against the installed torch."""
+    """The g++ line of the extension, against the installed torch."""
     import torch
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
     return ["g++", *HOST_FLAGS, "-shared", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
             f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING, "-o", out,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING, BINDING_CALLS, "-o", out,
             f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
@@ -87,7 +88,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         binding = binding_cmd(BINDING_OUT + ".tmp")
     except (ImportError, OSError) as e:  # OSError: a torch whose libraries do not load
         binding = None
-        print(f"without {os.path.basename(BINDING_OUT)} (lists of torch tensors): {e}", file=sys.stderr)
+        print(f"without {os.path.basename(BINDING_OUT)} (lists of torch tensors, activations): {e}", file=sys.stderr)
     jobs = jobs or min(len(cmds) + 1, max(1, (os.cpu_count() or 4)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         done = [ex.submit(_run, cmd) for cmd in cmds]
