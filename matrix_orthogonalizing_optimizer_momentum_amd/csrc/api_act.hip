@@ -41,7 +41,7 @@ bool bad_outputs(const Span* outs, int no, const Span* ins, int ni, const Span* 
 struct WgradPlan {
   bool copy_dz;
   int64_t npad, ldxt, lddz, dfull, ldp, xt, dzc, part, bytes;
-  int splits;
+  int splits, tile;
 };
 
 int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
@@ -54,24 +54,28 @@ int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
              : MUONH_OK;
 }
 
-// Parts of the tokens, by the time of the rounds of the chip in microseconds: a
-// stage of a tile 1.6, its epilogue 9; with several parts the second launch, and
-// the parts' sums written and read at 4 MB/us.
-int wgrad_splits(int64_t n, int64_t rows, int64_t width) {
-  const int64_t tiles = up(rows, kXTile) / kXTile * (up(width, kXTile) / kXTile), stages = up(n, kXStage) / kXStage;
-  double best = 0;
-  int splits = 1;
-  for (int64_t k = 1; k <= 64 && k <= stages; ++k) {
-    if (k > 1 && tiles * k > 2 * kXCus) break;
-    const double rounds = (double)((tiles * k + kXCus - 1) / kXCus);
-    double t = rounds * (1.6 * (double)((stages + k - 1) / k) + 9.0);
-    if (k > 1) t += 5.0 + 8.0 * (double)(k * rows) * (double)width / 4e6;
-    if (k == 1 || t < best) {
-      best = t;
-      splits = (int)k;
+// Tile and parts of the tokens.
+struct WgradChoice {
+  int tile, splits;
+};
+WgradChoice wgrad_choice(int64_t n, int64_t rows, int64_t width) {
+  const int64_t stages = up(n, kXStage) / kXStage;
+  WgradChoice best{kXTile, 1};
+  double least = 0;
+  for (const int tile : {256, 128, 64}) {
+    const int64_t tiles = up(rows, tile) / tile * (up(width, tile) / tile);
+    for (int64_t k = 1; k <= 64 && k <= std::max<int64_t>(stages, 1); ++k) {
+      if (k > 1 && tiles * k > 4 * kXCus) break;
+      const double rounds = (double)((tiles * k + kXCus - 1) / kXCus);
+      double t = rounds * (1.6 * (double)((stages + k - 1) / k) + 9.0);
+      if (k > 1) t += 5.0 + 8.0 * (double)(k * rows) * (double)width / 4e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = {tile, (int)k};
+      }
     }
   }
-  return splits;
+  return best;
 }
 
 WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
@@ -84,15 +88,18 @@ WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
   p.lddz = up(rows, 8);
   p.dfull = p.copy_dz ? 0 : n / kXStage * kXStage;
   p.ldp = up(width, 8);
-  p.splits = wgrad_splits(n, rows, width);
+  const WgradChoice c = wgrad_choice(n, rows, width);
+  p.tile = c.tile;
+  p.splits = c.splits;
+  const bool large = p.tile == kXTile;  // the others read the caller's buffers
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
     at += up(bytes, 256);
     return o;
   };
-  p.xt = take(n ? 2 * up(width, kXTile) * p.ldxt : 0);
-  p.dzc = take(2 * (p.npad - p.dfull) * p.lddz);
+  p.xt = take(large && n ? 2 * up(width, kXTile) * p.ldxt : 0);
+  p.dzc = take(!large ? 0 : 2 * (p.npad - p.dfull) * p.lddz);
   p.part = take(p.splits > 1 ? 4 * p.splits * rows * p.ldp : 0);
   p.bytes = std::max<int64_t>(at, 256);
   return p;
@@ -275,8 +282,9 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   a.dw_dt = internal_dtype(dw_dtype);
   a.accumulate = accumulate;
   a.splits = p.splits;
+  a.tile = p.tile;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  {
+  if (p.tile == kXTile) {
     ProfScope pf(s, PC_WPREP, 0, 3.0 * (double)n * (double)width);
     MUONH_TRY_HIP(launch_wgrad_prepare(a, s));
   }

@@ -77,41 +77,21 @@ __global__ __launch_bounds__(256) void k_wgrad_prepare(const WgradArgs a, int xt
   }
 }
 
-// One 256 x 256 tile over one part of the tokens.
-template <typename WT>
-__global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad(const WgradArgs a, int ni,
-                                                                                             int no) {
-  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
-  constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hi = lane >> 5;
-  const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
-  const int job = xcd_job(blockIdx.x, gridDim.x), per = ni * no, split = job / per;
-  int to, ti;
-  block_order(job - split * per, ni, no, ti, to);
-  const int64_t i0 = (int64_t)ti * kXTile, o0 = (int64_t)to * kXTile;
-  const int64_t all = a.npad / kXStage;
-  const int64_t s0 = all * split / a.splits, s1 = all * (split + 1) / a.splits;
-  const uint16_t* const xt = a.xt + i0 * a.ldxt + s0 * kXStage;
-  const uint16_t *const dz = a.dz + o0, *const dzc = a.dzc + o0;
-  const int64_t full = a.dfull, ld = a.lddz;
-  f32x16_t acc[MI][NI];
-  product<false, true, MI, NI>(
-      smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
-      [=](int s) {
-        const int64_t t = (s0 + s) * kXStage;
-        return t < full ? dz + t * ld : dzc + (t - full) * ld;
-      },
-      ld, ld - o0, acc);
+// Stores a wave's MI x NI blocks of 32 x 32 (columns from d0, rows from o0): into
+// dw, or as sums of one part of the tokens.
+template <typename WT, int MI, int NI>
+__device__ __forceinline__ void put_tile(const WgradArgs& a, int split, int64_t d0, int64_t o0, const f32x16_t (&acc)[MI][NI]) {
+  const int lane = threadIdx.x & 63, hi = lane >> 5;
   if (a.splits > 1) {
     float* const out = a.part + (int64_t)split * a.rows * a.ldp;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int64_t o = o0 + wn * WN + j * 32 + (lane & 31);
+      const int64_t o = o0 + j * 32 + (lane & 31);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t d = i0 + wm * WM + i * 32 + 8 * q + 4 * hi;
+          const int64_t d = d0 + i * 32 + 8 * q + 4 * hi;
           if (d >= a.ldp || o >= a.rows) continue;
           *reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(out + o * a.ldp + d)) =
               f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
@@ -124,7 +104,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int pq = 0; pq < 2; ++pq) {
-      const int64_t d = i0 + wm * WM + i * 32 + 16 * pq + 8 * hi;
+      const int64_t d = d0 + i * 32 + 16 * pq + 8 * hi;
       const int m = (int)min<int64_t>(max<int64_t>(a.width - d, 0), 8);
       float f[8];
 #pragma unroll
@@ -136,7 +116,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
       }
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        const int64_t o = o0 + wn * WN + j * 32 + (lane & 31);
+        const int64_t o = o0 + j * 32 + (lane & 31);
         float e[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -160,6 +140,194 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
         else store_first(dw, at, m, e);
       }
     }
+}
+
+// One 256 x 256 tile over one part of the tokens.
+template <typename WT>
+__global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad(const WgradArgs a, int ni,
+                                                                                             int no) {
+  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
+  constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
+  const int job = xcd_job(blockIdx.x, gridDim.x), per = ni * no, split = job / per;
+  int to, ti;
+  block_order(job - split * per, ni, no, ti, to);
+  const int64_t i0 = (int64_t)ti * kXTile, o0 = (int64_t)to * kXTile;
+  const int64_t all = a.npad / kXStage;
+  const int64_t s0 = all * split / a.splits, s1 = all * (split + 1) / a.splits;
+  const uint16_t* const xt = a.xt + i0 * a.ldxt + s0 * kXStage;
+  const uint16_t *const dz = a.dz + o0, *const dzc = a.dzc + o0;
+  const int64_t full = a.dfull, ld = a.lddz;
+  f32x16_t acc[MI][NI];
+  product<false, true, MI, NI>(
+      smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
+      [=](int s) {
+        const int64_t t = (s0 + s) * kXStage;
+        return t < full ? dz + t * ld : dzc + (t - full) * ld;
+      },
+      ld, ld - o0, acc);
+  put_tile<WT, MI, NI>(a, split, i0 + wm * WM, o0 + wn * WN, acc);
+}
+
+// A T x T tile over one part of the tokens, from the caller's buffers in one
+// launch: 4 waves of T/2 x T/2.  A stage of 64 tokens comes through registers (any
+// alignment; x is brought to bf16 there) into LDS as it lies, tokens down, and
+// both operands are read transposed.  Rows are padded by 64 bytes, so that the 4
+// tokens which a transposing read touches lie in different banks.  Two stages are
+// in flight in registers and one in LDS beside the one that is multiplied, with
+// one barrier a stage.  What lies behind a row's end is read as it comes (the next
+// row) and reaches only results that are not kept; stages whose reads would
+// leave a buffer are read value by value, with zeros behind the last token.
+constexpr int kDThreads = 256;
+template <typename WT, int T>
+__global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad_direct(const WgradArgs a, int ni,
+                                                                                                    int no) {
+  constexpr int P = T + 32, NB = T / 64;                      // pitch of a row in LDS; 32 x 32 blocks of a wave along a side
+  constexpr int XC = T / 16, XU = 64 * XC / kDThreads;        // chunks of 16 x values of a row, of a thread
+  constexpr int ZC = T / 8, ZU = 64 * ZC / kDThreads;         // chunks of 8 dz values
+  __shared__ __attribute__((aligned(16))) uint16_t sx[2][64 * P], sz[2][64 * P];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int job = xcd_job(blockIdx.x, gridDim.x), per = ni * no, split = job / per;
+  int to, ti;
+  block_order(job - split * per, ni, no, ti, to);
+  const int64_t i0 = (int64_t)ti * T, o0 = (int64_t)to * T, nblk = mx_blocks(a.width);
+  const int64_t all = (a.n + 63) / 64;
+  const int64_t s0 = all * split / a.splits, s1 = all * (split + 1) / a.splits;
+  // stages up to sf are read whole: their last row's chunks end inside the buffers
+  const int64_t room = min(min((a.n * a.width - i0 - T) / a.width, (a.n * a.rows - o0 - T) / a.rows),
+                           (a.n * nblk - (i0 + T) / kMxBlock) / nblk);  // rows 0 .. room - 1 may be followed by one more
+  const int64_t sf = max(s0, min(s1, (room + 1) / 64));
+  f32x16_t acc[NB][NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  struct Stage {
+    u32x4_t x[XU], z[ZU];
+    uint32_t f[XU];
+  };
+  const uint32_t vx = (uint32_t)((tid / XC) * a.width + tid % XC * 16), vz = (uint32_t)(((tid / ZC) * a.rows + tid % ZC * 8) * 2);
+  const uint32_t vf = (uint32_t)((tid / XC) * nblk + tid % XC / 2);
+  auto load = [&](int64_t s, Stage& r) {
+    const uint8_t *const px = a.q + s * 64 * a.width + i0, *const pf = a.scales + s * 64 * nblk + i0 / kMxBlock;
+    const char* const pz = reinterpret_cast<const char*>(a.dz + s * 64 * a.rows + o0);
+#pragma unroll
+    for (int u = 0; u < XU; ++u) {
+      r.x[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_b*>(gmem(px + u * (kDThreads / XC) * a.width) + vx);
+      r.f[u] = *(gmem(pf + u * (kDThreads / XC) * nblk) + vf);
+    }
+#pragma unroll
+    for (int u = 0; u < ZU; ++u)
+      r.z[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(pz + u * (kDThreads / ZC) * a.rows * 2) + vz);
+  };
+  // the same, value by value where a chunk is not whole; zeros behind the last token
+  auto load_edge = [&](int64_t s, Stage& r) {
+#pragma unroll
+    for (int u = 0; u < XU; ++u) {
+      const int id = tid + u * kDThreads;
+      const int64_t t = s * 64 + id / XC, c = i0 + id % XC * 16;
+      r.x[u] = u32x4_t{0u, 0u, 0u, 0u};
+      r.f[u] = 127;
+      if (t < a.n && c < a.width) {
+        const uint8_t* const p = a.q + t * a.width + c;
+        r.f[u] = gmem(a.scales)[t * nblk + c / kMxBlock];
+        if (c + 16 <= a.width) {
+          r.x[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_b*>(gmem(p));
+        } else {
+          const int m = (int)(a.width - c);
+          const u32x2_t lo = load_q8(p, min(m, 8)), up = load_q8(p + 8, max(m - 8, 0));
+          r.x[u] = u32x4_t{lo[0], lo[1], up[0], up[1]};
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < ZU; ++u) {
+      const int id = tid + u * kDThreads;
+      const int64_t t = s * 64 + id / ZC, c = o0 + id % ZC * 8;
+      r.z[u] = u32x4_t{0u, 0u, 0u, 0u};
+      if (t < a.n && c < a.rows) {
+        const uint16_t* const p = a.dz + t * a.rows + c;
+        if (c + 8 <= a.rows) {
+          r.z[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < a.rows) r.z[u][k / 2] |= (uint32_t)gmem(p)[k] << (16 * (k & 1));
+        }
+      }
+    }
+  };
+  auto store = [&](int buf, const Stage& r) {
+#pragma unroll
+    for (int u = 0; u < XU; ++u) {
+      const int id = tid + u * kDThreads;
+      uint16_t* const p = sx[buf] + id / XC * P + id % XC * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4_t*>(p + 8 * h) = e4m3_to_bf16(u32x2_t{r.x[u][2 * h], r.x[u][2 * h + 1]}, r.f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < ZU; ++u) {
+      const int id = tid + u * kDThreads;
+      *reinterpret_cast<u32x4_t*>(sz[buf] + id / ZC * P + id % ZC * 8) = r.z[u];
+    }
+  };
+  const int j16 = lane & 15, g = lane >> 4;
+  const int at = (8 * (g >> 1) + (j16 >> 2)) * P + 16 * (g & 1) + 4 * (j16 & 3);
+  const int wi = (wave >> 1) * (T / 2), wo = (wave & 1) * (T / 2);
+  auto fragment = [&](const uint16_t* base, int kk, int col) {
+    const uint16_t* p = base + at + kk * 16 * P + col;
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)p);
+    const i16x4_t up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p + 4 * P));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      bf16x8_t fa[NB], fb[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) fa[i] = fragment(sx[buf], kk, wi + 32 * i);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) fb[j] = fragment(sz[buf], kk, wo + 32 * j);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  // Stage s goes to buffer (s - s0) % 2; that buffer's readers, of stage s - 2, are
+  // behind the barrier of stage s - 1.
+  auto step = [&](int buf, Stage& r, int64_t next) {
+    store(buf, r);
+    load(min(next, sf - 1), r);
+    lds_release();
+    barrier();
+    lds_acquire();
+    multiply(buf);
+  };
+  if (s0 < sf) {
+    Stage even, odd;
+    load(s0, even);
+    load(min(s0 + 1, sf - 1), odd);
+    for (int64_t s = s0;;) {
+      step(0, even, s + 2);
+      if (++s == sf) break;
+      step(1, odd, s + 2);
+      if (++s == sf) break;
+    }
+  }
+  for (int64_t s = sf; s < s1; ++s) {
+    Stage r;
+    load_edge(s, r);
+    store((int)(s - s0) & 1, r);
+    __syncthreads();
+    multiply((int)(s - s0) & 1);
+  }
+  put_tile<WT, NB, NB>(a, split, i0 + wi, o0 + wo, acc);
 }
 
 // dw from the parts: 8 columns a thread.
@@ -203,17 +371,23 @@ hipError_t launch_wgrad_prepare(const WgradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
-  const int ni = (int)((a.width + kXTile - 1) / kXTile), no = (int)((a.rows + kXTile - 1) / kXTile);
+namespace {
+template <typename WT>
+hipError_t wgrad(const WgradArgs& a, hipStream_t s) {
+  const int ni = (int)((a.width + a.tile - 1) / a.tile), no = (int)((a.rows + a.tile - 1) / a.tile);
   const dim3 g((uint32_t)((int64_t)ni * no * a.splits));
-  if (a.dw_dt == DT_BF16) k_wgrad<bf16_t><<<g, kXThreads, 0, s>>>(a, ni, no);
-  else k_wgrad<float><<<g, kXThreads, 0, s>>>(a, ni, no);
-  hipError_t e = hipGetLastError();
+  if (a.tile == kXTile) k_wgrad<WT><<<g, kXThreads, 0, s>>>(a, ni, no);
+  else if (a.tile == 128) k_wgrad_direct<WT, 128><<<g, kDThreads, 0, s>>>(a, ni, no);
+  else k_wgrad_direct<WT, 64><<<g, kDThreads, 0, s>>>(a, ni, no);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const dim3 j((uint32_t)((a.rows * (a.ldp / 8) + 255) / 256));
-  if (a.dw_dt == DT_BF16) k_wgrad_join<bf16_t><<<j, 256, 0, s>>>(a);
-  else k_wgrad_join<float><<<j, 256, 0, s>>>(a);
+  k_wgrad_join<WT><<<dim3((uint32_t)((a.rows * (a.ldp / 8) + 255) / 256)), 256, 0, s>>>(a);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
+  return a.dw_dt == DT_BF16 ? wgrad<bf16_t>(a, s) : wgrad<float>(a, s);
 }
 
 }  // namespace muonh

@@ -70,6 +70,19 @@ __device__ __forceinline__ void from_e4m3(const u32x2_t q, float factor, float (
   }
 }
 
+// The same, rounded to bf16 (exact but for scales that this library does not write);
+// one conversion for two values.
+__device__ __forceinline__ u32x4_t e4m3_to_bf16(const u32x2_t q, uint32_t scale) {
+  const float f = __uint_as_float(scale << 23);
+  u32x4_t w;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[k], f, false));
+    w[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[k], f, true));
+  }
+  return w;
+}
+
 // 8 bytes at any address, or the first m of them (the others 0).
 __device__ __forceinline__ u32x2_t load_q8(const uint8_t* p) { return *reinterpret_cast<const MUONH_GLOBAL u32x2_b*>(gmem(p)); }
 __device__ __forceinline__ u32x2_t load_q8(const uint8_t* p, int m) {

@@ -21,7 +21,7 @@ struct WgradArgs {
   float* part;                       // [splits][rows][ldp], with splits > 1
   int64_t n, npad, rows, width, ldxt, lddz, dfull, ldp;
   float scale;
-  int32_t dw_dt, accumulate, splits;
+  int32_t dw_dt, accumulate, splits, tile;  // tile: 256 (from xt and dzc), or 128 or 64 from q and dz
 };
 
 hipError_t launch_wgrad_prepare(const WgradArgs& a, hipStream_t s);

@@ -156,3 +156,32 @@ def test_large_offsets():
     d = dz[rowsel].double()
     want, size = d.t() @ v, d.abs().t() @ v.abs()
     assert bool(((dw.double() - want).abs() <= 2 * U * 200 * size + U * want.abs()).all())
+
+
+@pytest.mark.parametrize("n", [256, 300])
+def test_every_code_and_scale(n):
+    """dz of ones at (t, t): dw is x, for every code under every scale byte."""
+    print(f"[case] weight gradient, every code and scale {n}", flush=True)
+    q = torch.zeros(n, 256, dtype=torch.uint8)
+    q[:256] = torch.arange(256, dtype=torch.uint8)
+    s = torch.full((n, 8), 127, dtype=torch.uint8)
+    s[:256] = torch.arange(256, dtype=torch.uint8)[:, None]
+    p = (q.to(DEV).view(torch.float8_e4m3fn), s.to(DEV).view(torch.float8_e8m0fnu))
+    want = mm.mx_unpack(p).float()  # rounded to bf16
+    for t in range(0, 256, 64):  # 64 tokens at a time, so that no NaN or infinity of another token is in the sum
+        one = (p[0][t:t + 64].contiguous(), p[1][t:t + 64].contiguous())
+        for rows in (64, 130):
+            for k in range(0, 64, 16):
+                dz = torch.zeros(64, rows, dtype=BF16, device=DEV)
+                dz[k, 0] = 1.0
+                got = mm.weight_grad(dz, one, out_dtype=F32)[0]
+                finite = want[t:t + 64].isfinite().all(0)
+                assert torch.equal(got[finite], want[t + k][finite])
+    # a token alone, NaN and infinity among its values
+    for t in list(range(0, 256, 15)) + [254, 255]:
+        one = (p[0][t:t + 1].contiguous(), p[1][t:t + 1].contiguous())
+        got = mm.weight_grad(torch.ones(1, 1, dtype=BF16, device=DEV), one, out_dtype=F32)[0]
+        assert torch.equal(got.isnan(), want[t].isnan())
+        low = want[t].abs() < 2.0 ** -126  # the matrix cores may take such operands as zero
+        assert torch.equal(got.nan_to_num(nan=0.0)[~low], want[t].nan_to_num(nan=0.0)[~low])
+        assert bool((got[low].abs() <= 2.0 ** -126).all())
