@@ -40,7 +40,7 @@ bool bad_outputs(const Span* outs, int no, const Span* ins, int ni, const Span* 
 // ------------------------------------------------------------ weight gradient
 struct WgradPlan {
   bool copy_dz;
-  int64_t npad, ldxt, lddz, dfull, ldp, xt, dzc, part, bytes;
+  int64_t npad, ldxt, lddz, dfull, ldp, whole, xt, dzc, part, bytes;
   int splits, tile;
 };
 
@@ -80,6 +80,15 @@ WgradChoice wgrad_choice(int64_t n, int64_t rows, int64_t width) {
 
 WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
   WgradPlan p{};
+  const WgradChoice c = wgrad_choice(n, rows, width);
+  p.tile = c.tile;
+  p.splits = c.splits;
+  // The smaller tiles' reads run over a row's end by less than a tile: the last
+  // rows that this leaves the buffers from are in stages read value by value.
+  auto behind = [&](int64_t row, int64_t over) { return (over + row - 1) / row; };
+  const int64_t tail = std::max({behind(width, up(width, c.tile) - width), behind(rows, up(rows, c.tile) - rows),
+                                 behind(mx_blocks(width), up(width, c.tile) / kMxBlock - mx_blocks(width))});
+  p.whole = std::max<int64_t>(0, n - tail) / kXStage;
   // dz is an operand as it stands when its rows are on a 16-byte grid, but for
   // the rows of its last, partial stage; else the call works on a padded copy
   p.copy_dz = rows % 8 != 0 || misaligned(dz, 16);
@@ -88,9 +97,6 @@ WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
   p.lddz = up(rows, 8);
   p.dfull = p.copy_dz ? 0 : n / kXStage * kXStage;
   p.ldp = up(width, 8);
-  const WgradChoice c = wgrad_choice(n, rows, width);
-  p.tile = c.tile;
-  p.splits = c.splits;
   const bool large = p.tile == kXTile;  // the others read the caller's buffers
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -278,6 +284,7 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   a.lddz = p.lddz;
   a.dfull = p.dfull;
   a.ldp = p.ldp;
+  a.whole = p.whole;
   a.scale = scale;
   a.dw_dt = internal_dtype(dw_dtype);
   a.accumulate = accumulate;

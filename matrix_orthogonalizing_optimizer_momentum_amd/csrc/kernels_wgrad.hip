@@ -154,8 +154,8 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   int to, ti;
   block_order(job - split * per, ni, no, ti, to);
   const int64_t i0 = (int64_t)ti * kXTile, o0 = (int64_t)to * kXTile;
-  const int64_t all = a.npad / kXStage;
-  const int64_t s0 = all * split / a.splits, s1 = all * (split + 1) / a.splits;
+  const int all = (int)(a.npad / kXStage);
+  const int64_t s0 = (uint32_t)(all * split) / (uint32_t)a.splits, s1 = (uint32_t)(all * (split + 1)) / (uint32_t)a.splits;
   const uint16_t* const xt = a.xt + i0 * a.ldxt + s0 * kXStage;
   const uint16_t *const dz = a.dz + o0, *const dzc = a.dzc + o0;
   const int64_t full = a.dfull, ld = a.lddz;
@@ -192,12 +192,9 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   int to, ti;
   block_order(job - split * per, ni, no, ti, to);
   const int64_t i0 = (int64_t)ti * T, o0 = (int64_t)to * T, nblk = mx_blocks(a.width);
-  const int64_t all = (a.n + 63) / 64;
-  const int64_t s0 = all * split / a.splits, s1 = all * (split + 1) / a.splits;
-  // stages up to sf are read whole: their last row's chunks end inside the buffers
-  const int64_t room = min(min((a.n * a.width - i0 - T) / a.width, (a.n * a.rows - o0 - T) / a.rows),
-                           (a.n * nblk - (i0 + T) / kMxBlock) / nblk);  // rows 0 .. room - 1 may be followed by one more
-  const int64_t sf = max(s0, min(s1, (room + 1) / 64));
+  const int all = (int)((a.n + 63) / 64);
+  const int s0 = (int)((uint32_t)(all * split) / (uint32_t)a.splits), s1 = (int)((uint32_t)(all * (split + 1)) / (uint32_t)a.splits);
+  const int sf = max(s0, min(s1, (int)a.whole));
   f32x16_t acc[NB][NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -210,21 +207,38 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     u32x4_t x[XU], z[ZU];
     uint32_t f[XU];
   };
-  const uint32_t vx = (uint32_t)((tid / XC) * a.width + tid % XC * 16), vz = (uint32_t)(((tid / ZC) * a.rows + tid % ZC * 8) * 2);
-  const uint32_t vf = (uint32_t)((tid / XC) * nblk + tid % XC / 2);
-  auto load = [&](int64_t s, Stage& r) {
-    const uint8_t *const px = a.q + s * 64 * a.width + i0, *const pf = a.scales + s * 64 * nblk + i0 / kMxBlock;
-    const char* const pz = reinterpret_cast<const char*>(a.dz + s * 64 * a.rows + o0);
+  // this thread's chunks, from the first value of the next stage to be loaded
+  uint32_t vx[XU], vf[XU], vz[ZU];
+#pragma unroll
+  for (int u = 0; u < XU; ++u) {
+    const int id = tid + u * kDThreads;
+    vx[u] = (uint32_t)((id / XC) * a.width + id % XC * 16);
+    vf[u] = (uint32_t)((id / XC) * nblk + id % XC / 2);
+  }
+#pragma unroll
+  for (int u = 0; u < ZU; ++u) {
+    const int id = tid + u * kDThreads;
+    vz[u] = (uint32_t)(((id / ZC) * a.rows + id % ZC * 8) * 2);
+  }
+  const MUONH_GLOBAL uint8_t* px = gmem(a.q + (int64_t)s0 * 64 * a.width + i0);
+  const MUONH_GLOBAL uint8_t* pf = gmem(a.scales + (int64_t)s0 * 64 * nblk + i0 / kMxBlock);
+  const MUONH_GLOBAL char* pz = reinterpret_cast<const MUONH_GLOBAL char*>(gmem(a.dz + (int64_t)s0 * 64 * a.rows + o0));
+  const int64_t ax = 64 * a.width, af = 64 * nblk, az = 128 * a.rows;
+  // the next stage (the last one again behind it)
+  auto load = [&](Stage& r, bool more) {
 #pragma unroll
     for (int u = 0; u < XU; ++u) {
-      r.x[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_b*>(gmem(px + u * (kDThreads / XC) * a.width) + vx);
-      r.f[u] = *(gmem(pf + u * (kDThreads / XC) * nblk) + vf);
+      r.x[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_b*>(px + vx[u]);
+      r.f[u] = pf[vf[u]];
     }
 #pragma unroll
-    for (int u = 0; u < ZU; ++u)
-      r.z[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(pz + u * (kDThreads / ZC) * a.rows * 2) + vz);
+    for (int u = 0; u < ZU; ++u) r.z[u] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(pz + vz[u]);
+    px += more ? ax : 0;
+    pf += more ? af : 0;
+    pz += more ? az : 0;
+    __builtin_amdgcn_sched_barrier(0);  // the waits count loads in this order
   };
-  // the same, value by value where a chunk is not whole; zeros behind the last token
+  // a stage value by value where a chunk is not whole; zeros behind the last token
   auto load_edge = [&](int64_t s, Stage& r) {
 #pragma unroll
     for (int u = 0; u < XU; ++u) {
@@ -285,25 +299,36 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     const i16x4_t up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p + 4 * P));
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
   };
+  // all fragments of half a stage are on their way while the other half is multiplied
   auto multiply = [&](int buf) {
+    bf16x8_t fa[2][2][NB], fb[2][2][NB];
+    auto read = [&](int h) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      bf16x8_t fa[NB], fb[NB];
+      for (int q = 0; q < 2; ++q) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) fa[i] = fragment(sx[buf], kk, wi + 32 * i);
+        for (int i = 0; i < NB; ++i) fa[h][q][i] = fragment(sx[buf], 2 * h + q, wi + 32 * i);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) fb[j] = fragment(sz[buf], kk, wo + 32 * j);
+        for (int j = 0; j < NB; ++j) fb[h][q][j] = fragment(sz[buf], 2 * h + q, wo + 32 * j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    read(0);
+    read(1);
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[h][q][i], fb[h][q][j], acc[i][j], 0, 0, 0);
   };
   // Stage s goes to buffer (s - s0) % 2; that buffer's readers, of stage s - 2, are
   // behind the barrier of stage s - 1.
-  auto step = [&](int buf, Stage& r, int64_t next) {
+  auto step = [&](int buf, Stage& r, int next) {
     store(buf, r);
-    load(min(next, sf - 1), r);
+    load(r, next + 1 < sf);
     lds_release();
     barrier();
     lds_acquire();
@@ -311,21 +336,21 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   };
   if (s0 < sf) {
     Stage even, odd;
-    load(s0, even);
-    load(min(s0 + 1, sf - 1), odd);
-    for (int64_t s = s0;;) {
+    load(even, s0 + 1 < sf);
+    load(odd, s0 + 2 < sf);
+    int s = s0;
+    for (; s + 1 < sf; s += 2) {
       step(0, even, s + 2);
-      if (++s == sf) break;
-      step(1, odd, s + 2);
-      if (++s == sf) break;
+      step(1, odd, s + 3);
     }
+    if (s < sf) step(0, even, s + 2);
   }
-  for (int64_t s = sf; s < s1; ++s) {
+  for (int s = sf; s < s1; ++s) {
     Stage r;
     load_edge(s, r);
-    store((int)(s - s0) & 1, r);
+    store((s - s0) & 1, r);
     __syncthreads();
-    multiply((int)(s - s0) & 1);
+    multiply((s - s0) & 1);
   }
   put_tile<WT, NB, NB>(a, split, i0 + wi, o0 + wo, acc);
 }

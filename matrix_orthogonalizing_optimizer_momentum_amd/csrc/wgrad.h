@@ -20,6 +20,7 @@ struct WgradArgs {
   uint16_t* dzc;                     // dz's rows [dfull, n), padded with zeros to a whole stage, of lddz
   float* part;                       // [splits][rows][ldp], with splits > 1
   int64_t n, npad, rows, width, ldxt, lddz, dfull, ldp;
+  int64_t whole;                     // stages that the 64 and 128 tiles read whole, over the rows' ends
   float scale;
   int32_t dw_dt, accumulate, splits, tile;  // tile: 256 (from xt and dzc), or 128 or 64 from q and dz
 };
