@@ -54,21 +54,35 @@ int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
              : MUONH_OK;
 }
 
-// Tile and parts of the tokens.
+// Tile and parts of the tokens, by an estimate of the call's time in microseconds,
+// within some 15% of what these took (8192 x 2304 x 768: 256 tiles in 9 parts 59, 128
+// in 4 parts 53, 64 whole 55; 2048 x 768 x 768: 35, 19 and 14; 512 x 4096 x 4096: 37,
+// 36 and 51; 2048 x 14336 x 4096: 245, 284).  A stage of 64 tokens of a 256 tile
+// takes 1.75 on its own compute unit, with x brought to bf16 by a launch before it
+// (3 bytes a value); of a 128 tile 0.72, or 0.5 each where several share a unit; of
+// a 64 tile 0.28.  Each tile has an epilogue, the result is stored at 5 GB/ms, and
+// parts cost a launch and are written and read.
 struct WgradChoice {
   int tile, splits;
 };
 WgradChoice wgrad_choice(int64_t n, int64_t rows, int64_t width) {
   const int64_t stages = up(n, kXStage) / kXStage;
+  const double values = (double)rows * (double)width;
   WgradChoice best{kXTile, 1};
   double least = 0;
   for (const int tile : {256, 128, 64}) {
     const int64_t tiles = up(rows, tile) / tile * (up(width, tile) / tile);
-    for (int64_t k = 1; k <= 64 && k <= std::max<int64_t>(stages, 1); ++k) {
+    if (tile != kXTile && tiles > 64 * kXCus) continue;
+    for (int64_t k = 1; k <= 32 && k <= std::max<int64_t>(stages, 1); ++k) {
       if (k > 1 && tiles * k > 4 * kXCus) break;
-      const double rounds = (double)((tiles * k + kXCus - 1) / kXCus);
-      double t = rounds * (1.6 * (double)((stages + k - 1) / k) + 9.0);
-      if (k > 1) t += 5.0 + 8.0 * (double)(k * rows) * (double)width / 4e6;
+      const double each = (double)((stages + k - 1) / k);
+      // tiles of the busiest unit; many tiles even out
+      const double c = tiles * k > 4 * kXCus ? (double)(tiles * k) / kXCus : (double)((tiles * k + kXCus - 1) / kXCus);
+      double t = 2.0 * values / 5e6;
+      if (tile == 256) t += 8.0 + 3.0 * (double)n * (double)width / 3.5e6 + c * (1.75 * each + 5.0);
+      else if (tile == 128) t += 3.5 + (c > 1 ? 0.5 * c : 0.72) * each + 1.5 * (c + 1);
+      else t += 4.0 + c * (0.28 * each + 0.7);
+      if (k > 1) t += 3.0 + 8.0 * (double)k * values / 6e6;
       if (least == 0 || t < least) {
         least = t;
         best = {tile, (int)k};

@@ -171,10 +171,13 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 }
 
 // A T x T tile over one part of the tokens, from the caller's buffers in one
-// launch: 4 waves of T/2 x T/2.  A stage of 64 tokens comes through registers (any
+// launch, by 4 waves.  A stage of 64 tokens comes through registers (any
 // alignment; x is brought to bf16 there) into LDS as it lies, tokens down, and
 // both operands are read transposed.  Rows are padded by 64 bytes, so that the 4
-// tokens which a transposing read touches lie in different banks.  Two stages are
+// tokens which a transposing read touches lie in different banks.  Those reads (64
+// bytes a clock) bound the loop, so a wave multiplies 64 x 64: a quarter of a tile
+// of 128, or a whole tile of 64 for a quarter of the tokens, with the waves' sums
+// joined at the end.  Two stages are
 // in flight in registers and one in LDS beside the one that is multiplied, with
 // one barrier a stage.  What lies behind a row's end is read as it comes (the next
 // row) and reaches only results that are not kept; stages whose reads would
@@ -183,11 +186,14 @@ constexpr int kDThreads = 256;
 template <typename WT, int T>
 __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad_direct(const WgradArgs a, int ni,
                                                                                                     int no) {
-  constexpr int P = T + 32, NB = T / 64;                      // pitch of a row in LDS; 32 x 32 blocks of a wave along a side
+  constexpr bool kWhole = T == 64;                            // a wave multiplies the whole tile
+  constexpr int P = T + 32, NB = 2;                           // pitch of a row in LDS; 32 x 32 blocks of a wave along a side
   constexpr int XC = T / 16, XU = 64 * XC / kDThreads;        // chunks of 16 x values of a row, of a thread
   constexpr int ZC = T / 8, ZU = 64 * ZC / kDThreads;         // chunks of 8 dz values
-  __shared__ __attribute__((aligned(16))) uint16_t sx[2][64 * P], sz[2][64 * P];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) uint16_t smem[4 * 64 * P];
+  uint16_t (*const sx)[64 * P] = reinterpret_cast<uint16_t (*)[64 * P]>(smem);
+  uint16_t (*const sz)[64 * P] = sx + 2;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int job = xcd_job(blockIdx.x, gridDim.x), per = ni * no, split = job / per;
   int to, ti;
   block_order(job - split * per, ni, no, ti, to);
@@ -292,37 +298,32 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   };
   const int j16 = lane & 15, g = lane >> 4;
   const int at = (8 * (g >> 1) + (j16 >> 2)) * P + 16 * (g & 1) + 4 * (j16 & 3);
-  const int wi = (wave >> 1) * (T / 2), wo = (wave & 1) * (T / 2);
+  const int wi = kWhole ? 0 : (wave >> 1) * 64, wo = kWhole ? 0 : (wave & 1) * 64;
   auto fragment = [&](const uint16_t* base, int kk, int col) {
     const uint16_t* p = base + at + kk * 16 * P + col;
     const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)p);
     const i16x4_t up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p + 4 * P));
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  // all fragments of half a stage are on their way while the other half is multiplied
   auto multiply = [&](int buf) {
-    bf16x8_t fa[2][2][NB], fb[2][2][NB];
-    auto read = [&](int h) {
+    constexpr int K = kWhole ? 1 : 4;                         // steps of 16 tokens that a wave takes of a stage
+    bf16x8_t fa[K][NB], fb[K][NB];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < K; ++q) {
+      const int kk = kWhole ? wave : q;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) fa[h][q][i] = fragment(sx[buf], 2 * h + q, wi + 32 * i);
+      for (int i = 0; i < NB; ++i) fa[q][i] = fragment(sx[buf], kk, wi + 32 * i);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) fb[h][q][j] = fragment(sz[buf], 2 * h + q, wo + 32 * j);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    read(0);
-    read(1);
+      for (int j = 0; j < NB; ++j) fb[q][j] = fragment(sz[buf], kk, wo + 32 * j);
+      if (q & 1) __builtin_amdgcn_sched_barrier(0);           // half a stage's reads are on their way before any product
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int q = 0; q < K; ++q)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[h][q][i], fb[h][q][j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[q][i], fb[q][j], acc[i][j], 0, 0, 0);
   };
   // Stage s goes to buffer (s - s0) % 2; that buffer's readers, of stage s - 2, are
   // behind the barrier of stage s - 1.
@@ -352,38 +353,79 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     __syncthreads();
     multiply((s - s0) & 1);
   }
-  put_tile<WT, NB, NB>(a, split, i0 + wi, o0 + wo, acc);
+  if constexpr (!kWhole) {
+    put_tile<WT, NB, NB>(a, split, i0 + wi, o0 + wo, acc);
+  } else {
+    // each wave takes one block of the tile from the others, in the order of the waves
+    static_assert(12 * 4096 <= 4 * 64 * P * 2, "three blocks a wave");
+    f32x4_t* const sh = reinterpret_cast<f32x4_t*>(smem);
+    __syncthreads();
+    f32x16_t mine[1][1];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const f32x16_t& v = acc[b >> 1][b & 1];
+      if (b == wave) {
+        mine[0][0] = v;
+      } else {
+        f32x4_t* const to_b = sh + (b * 3 + (wave < b ? wave : wave - 1)) * 256 + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) to_b[64 * q] = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t e = sh[(wave * 3 + k) * 256 + 64 * q + lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mine[0][0][4 * q + r] += e[r];
+      }
+    put_tile<WT, 1, 1>(a, split, i0 + 32 * (wave >> 1), o0 + 32 * (wave & 1), mine);
+  }
 }
 
-// dw from the parts: 8 columns a thread.
+// dw from the parts: 4 columns a thread, 8 parts in flight, added in their order.
 template <typename WT>
 __global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a) {
-  const int64_t per = a.ldp / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= per * a.rows) return;
-  const int64_t o = id / per, d = (id - o * per) * 8;
-  const int m = (int)min<int64_t>(a.width - d, 8);
+  const uint32_t per = (uint32_t)(a.ldp / 4), id = blockIdx.x * 256 + threadIdx.x;
+  const int64_t o = id / per, d = (int64_t)(id % per) * 4;
+  if (o >= a.rows) return;
+  const int m = (int)min<int64_t>(a.width - d, 4);
   if (m <= 0) return;
-  float e[8], p[8], f[8];
-  load8(a.part, o * a.ldp + d, e);
-  for (int k = 1; k < a.splits; ++k) {
-    load8(a.part, ((int64_t)k * a.rows + o) * a.ldp + d, p);
+  const int64_t step = a.rows * a.ldp;
+  const float* p = a.part + o * a.ldp + d;
+  f32x4_t e = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < a.splits; k += 8, p += 8 * step) {
+    f32x4_t r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] += p[j];
+    for (int u = 0; u < 8; ++u)
+      if (k + u < a.splits) r[u] = *reinterpret_cast<const MUONH_GLOBAL f32x4_t*>(gmem(p + u * step));
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k + u < a.splits) e += r[u];
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = 1.f;
-  if (a.gain != nullptr) load_first(a.gain, d, m, f);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] *= a.scale * f[j];
   WT* const dw = static_cast<WT*>(a.dw);
   const int64_t at = o * a.width + d;
-  if (a.accumulate) {
-    load_first(dw, at, m, p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] += p[j];
+  for (int j = 0; j < 4; ++j)
+    if (j < m) {
+      e[j] *= a.gain != nullptr ? a.scale * gmem(a.gain)[d + j] : a.scale;
+      if (a.accumulate) e[j] += St<WT>::ld(dw, at + j);
+    }
+  if (m == 4) {
+    if constexpr (sizeof(WT) == 4) {
+      typedef f32x4_t __attribute__((aligned(4))) f32x4_a;
+      *reinterpret_cast<MUONH_GLOBAL f32x4_a*>(gmem(dw + at)) = e;
+    } else {
+      typedef u32x2_t __attribute__((aligned(2))) u32x2_a;
+      *reinterpret_cast<MUONH_GLOBAL u32x2_a*>(gmem(dw + at)) = u32x2_t{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < m) St<WT>::st(dw, at + j, e[j]);
   }
-  if (m == 8) store8_any(dw, at, e);
-  else store_first(dw, at, m, e);
 }
 
 }  // namespace
@@ -406,7 +448,7 @@ hipError_t wgrad(const WgradArgs& a, hipStream_t s) {
   else k_wgrad_direct<WT, 64><<<g, kDThreads, 0, s>>>(a, ni, no);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  k_wgrad_join<WT><<<dim3((uint32_t)((a.rows * (a.ldp / 8) + 255) / 256)), 256, 0, s>>>(a);
+  k_wgrad_join<WT><<<dim3((uint32_t)((a.rows * (a.ldp / 4) + 255) / 256)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 }  // namespace
