@@ -58,10 +58,10 @@ int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
 // within some 15% of what these took (8192 x 2304 x 768: 256 tiles in 9 parts 59, 128
 // in 4 parts 53, 64 whole 55; 2048 x 768 x 768: 35, 19 and 14; 512 x 4096 x 4096: 37,
 // 36 and 51; 2048 x 14336 x 4096: 245, 284).  A stage of 64 tokens of a 256 tile
-// takes 1.75 on its own compute unit, with x brought to bf16 by a launch before it
-// (3 bytes a value); of a 128 tile 0.72, or 0.5 each where several share a unit; of
-// a 64 tile 0.28.  Each tile has an epilogue, the result is stored at 5 GB/ms, and
-// parts cost a launch and are written and read.
+// takes 1.55 on its own compute unit, with x brought to bf16 by a launch before it
+// (3 bytes a value); of a 128 tile 0.72, or 1.1 of the two that share a unit; of a 64
+// tile 0.28.  Each tile has an epilogue, the result is stored at 5 GB/ms (2.5
+// from the registers of a 256 tile), and parts cost a launch and are written and read.
 struct WgradChoice {
   int tile, splits;
 };
@@ -78,10 +78,10 @@ WgradChoice wgrad_choice(int64_t n, int64_t rows, int64_t width) {
       const double each = (double)((stages + k - 1) / k);
       // tiles of the busiest unit; many tiles even out
       const double c = tiles * k > 4 * kXCus ? (double)(tiles * k) / kXCus : (double)((tiles * k + kXCus - 1) / kXCus);
-      double t = 2.0 * values / 5e6;
-      if (tile == 256) t += 8.0 + 3.0 * (double)n * (double)width / 3.5e6 + c * (1.75 * each + 5.0);
-      else if (tile == 128) t += 3.5 + (c > 1 ? 0.5 * c : 0.72) * each + 1.5 * (c + 1);
-      else t += 4.0 + c * (0.28 * each + 0.7);
+      double t;
+      if (tile == 256) t = 8.0 + 3.0 * (double)n * (double)width / 3.5e6 + c * (1.55 * each + 5.0) + 2.0 * values / 2.5e6;
+      else if (tile == 128) t = 3.5 + (c > 4 ? 0.55 * c : c == 1 ? 0.72 : c == 2 ? 1.1 : c == 3 ? 1.82 : 2.2) * each + 0.8 * (c + 1) + 2.0 * values / 5e6;
+      else t = 3.2 + c * (0.28 * each + 0.6) + 2.0 * values / 5e6;
       if (k > 1) t += 3.0 + 8.0 * (double)k * values / 6e6;
       if (least == 0 || t < least) {
         least = t;

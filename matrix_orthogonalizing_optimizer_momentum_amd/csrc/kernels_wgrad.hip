@@ -77,6 +77,8 @@ __global__ __launch_bounds__(256) void k_wgrad_prepare(const WgradArgs a, int xt
   }
 }
 
+constexpr int kDThreads = 256;
+
 // Stores a wave's MI x NI blocks of 32 x 32 (columns from d0, rows from o0): into
 // dw, or as sums of one part of the tokens.
 template <typename WT, int MI, int NI>
@@ -170,6 +172,73 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   put_tile<WT, MI, NI>(a, split, i0 + wm * WM, o0 + wn * WN, acc);
 }
 
+// Puts a wave's NI x NJ blocks at (di, dj) of the tile in LDS: rows of T + 4 values
+// along the width.
+template <int T, int NI, int NJ>
+__device__ __forceinline__ void stage_tile(float* tile, int di, int dj, const f32x16_t (&acc)[NI][NJ]) {
+  const int lane = threadIdx.x & 63, hi = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(tile + (dj + 32 * j + (lane & 31)) * (T + 4) + di + 32 * i + 8 * q + 4 * hi) =
+            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+}
+
+// Stores a tile from LDS by whole rows (from the registers a store instruction would
+// reach 32 bytes of each of 32 rows).
+template <typename WT, int T>
+__device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t i0, int64_t o0, const float* tile) {
+  constexpr int C = T / 8, R = kDThreads / C;                 // chunks of a row, rows at a time
+  const int c = threadIdx.x % C * 8, r0 = threadIdx.x / C;
+  const int64_t d = i0 + c;
+  auto row = [&](int r, float (&e)[8]) {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c);
+    const f32x4_t up = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      e[k] = lo[k];
+      e[4 + k] = up[k];
+    }
+  };
+  float e[8];
+  if (a.splits > 1) {
+    float* const out = a.part + (int64_t)split * a.rows * a.ldp;
+    if (d >= a.ldp) return;
+#pragma unroll 2
+    for (int r = r0; r < T && o0 + r < a.rows; r += R) {
+      row(r, e);
+      store8(out, (o0 + r) * a.ldp + d, e);
+    }
+    return;
+  }
+  const int m = (int)min<int64_t>(a.width - d, 8);
+  if (m <= 0) return;
+  float f[8];
+  if (a.gain != nullptr) load_first(a.gain, d, m, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = a.gain != nullptr ? a.scale * f[k] : a.scale;
+  WT* const dw = static_cast<WT*>(a.dw);
+#pragma unroll 2
+  for (int r = r0; r < T && o0 + r < a.rows; r += R) {
+    const int64_t at = (o0 + r) * a.width + d;
+    row(r, e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] *= f[k];
+    if (a.accumulate) {
+      float old[8];
+      if (m == 8) load8_any(dw, at, old);
+      else load_first(dw, at, m, old);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] += old[k];
+    }
+    if (m == 8) store8_any(dw, at, e);
+    else store_first(dw, at, m, e);
+  }
+}
+
 // A T x T tile over one part of the tokens, from the caller's buffers in one
 // launch, by 4 waves.  A stage of 64 tokens comes through registers (any
 // alignment; x is brought to bf16 there) into LDS as it lies, tokens down, and
@@ -182,7 +251,6 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 // one barrier a stage.  What lies behind a row's end is read as it comes (the next
 // row) and reaches only results that are not kept; stages whose reads would
 // leave a buffer are read value by value, with zeros behind the last token.
-constexpr int kDThreads = 256;
 template <typename WT, int T>
 __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad_direct(const WgradArgs a, int ni,
                                                                                                     int no) {
@@ -353,8 +421,11 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     __syncthreads();
     multiply((s - s0) & 1);
   }
+  static_assert(T * (T + 4) * 4 <= 4 * 64 * P * 2, "the tile's sums fit the operands' place");
+  float* const tile = reinterpret_cast<float*>(smem);
   if constexpr (!kWhole) {
-    put_tile<WT, NB, NB>(a, split, i0 + wi, o0 + wo, acc);
+    __syncthreads();
+    stage_tile<T>(tile, wi, wo, acc);
   } else {
     // each wave takes one block of the tile from the others, in the order of the waves
     static_assert(12 * 4096 <= 4 * 64 * P * 2, "three blocks a wave");
@@ -381,8 +452,11 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
         for (int r = 0; r < 4; ++r) mine[0][0][4 * q + r] += e[r];
       }
-    put_tile<WT, 1, 1>(a, split, i0 + 32 * (wave >> 1), o0 + 32 * (wave & 1), mine);
+    __syncthreads();
+    stage_tile<T>(tile, 32 * (wave >> 1), 32 * (wave & 1), mine);
   }
+  __syncthreads();
+  put_rows<WT, T>(a, split, i0, o0, tile);
 }
 
 // dw from the parts: 4 columns a thread, 8 parts in flight, added in their order.
