@@ -211,7 +211,7 @@ int muonh_rms_norm_grad(const void* dy, int dy_dtype, const void* x, const void*
   a.gain = gain;
   a.dres = dres;
   a.dx = dx;
-  a.part = dgain ? static_cast<float*>(workspace) : nullptr;
+  a.part = dgain && !norm_grad_columns(n, width) ? static_cast<float*>(workspace) : nullptr;
   a.dgain = dgain;
   a.n = n;
   a.width = width;
