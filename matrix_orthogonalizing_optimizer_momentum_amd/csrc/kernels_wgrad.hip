@@ -79,76 +79,79 @@ __global__ __launch_bounds__(256) void k_wgrad_prepare(const WgradArgs a, int xt
 
 constexpr int kDThreads = 256;
 
-// Stores a wave's MI x NI blocks of 32 x 32 (columns from d0, rows from o0): into
-// dw, or as sums of one part of the tokens.
-template <typename WT, int MI, int NI>
-__device__ __forceinline__ void put_tile(const WgradArgs& a, int split, int64_t d0, int64_t o0, const f32x16_t (&acc)[MI][NI]) {
+// Puts a wave's NI x NJ blocks at (di, dj) of the tile in LDS: rows of T + 4 values
+// along the width.
+template <int T, int NI, int NJ>
+__device__ __forceinline__ void stage_tile(float* tile, int di, int dj, const f32x16_t (&acc)[NI][NJ]) {
   const int lane = threadIdx.x & 63, hi = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(tile + (dj + 32 * j + (lane & 31)) * (T + 4) + di + 32 * i + 8 * q + 4 * hi) =
+            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+}
+
+// Stores ROWS rows of a tile from LDS by whole rows (from the registers a store
+// instruction would reach 32 bytes of each of 32 rows).
+template <typename WT, int T, int ROWS, int THREADS>
+__device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t i0, int64_t o0, const float* tile) {
+  constexpr int C = T / 8, R = THREADS / C;                   // chunks of a row, rows at a time
+  const int c = threadIdx.x % C * 8, r0 = threadIdx.x / C;
+  const int64_t d = i0 + c;
+  auto row = [&](int r, float (&e)[8]) {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c);
+    const f32x4_t up = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      e[k] = lo[k];
+      e[4 + k] = up[k];
+    }
+  };
+  float e[8];
   if (a.splits > 1) {
     float* const out = a.part + (int64_t)split * a.rows * a.ldp;
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int64_t o = o0 + j * 32 + (lane & 31);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t d = d0 + i * 32 + 8 * q + 4 * hi;
-          if (d >= a.ldp || o >= a.rows) continue;
-          *reinterpret_cast<MUONH_GLOBAL f32x4_t*>(gmem(out + o * a.ldp + d)) =
-              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        }
+    if (d >= a.ldp) return;
+#pragma unroll 2
+    for (int r = r0; r < ROWS && o0 + r < a.rows; r += R) {
+      row(r, e);
+      store8(out, (o0 + r) * a.ldp + d, e);
     }
     return;
   }
+  const int m = (int)min<int64_t>(a.width - d, 8);
+  if (m <= 0) return;
+  float f[8];
+  if (a.gain != nullptr) load_first(a.gain, d, m, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = a.gain != nullptr ? a.scale * f[k] : a.scale;
   WT* const dw = static_cast<WT*>(a.dw);
+#pragma unroll 2
+  for (int r = r0; r < ROWS && o0 + r < a.rows; r += R) {
+    const int64_t at = (o0 + r) * a.width + d;
+    row(r, e);
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int k = 0; k < 8; ++k) e[k] *= f[k];
+    if (a.accumulate) {
+      float old[8];
+      if (m == 8) load8_any(dw, at, old);
+      else load_first(dw, at, m, old);
 #pragma unroll
-    for (int pq = 0; pq < 2; ++pq) {
-      const int64_t d = d0 + i * 32 + 16 * pq + 8 * hi;
-      const int m = (int)min<int64_t>(max<int64_t>(a.width - d, 0), 8);
-      float f[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = a.scale;
-      if (a.gain != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < m) f[k] *= gmem(a.gain)[d + k];
-      }
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int64_t o = o0 + j * 32 + (lane & 31);
-        float e[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * pq + k]),
-                                                           __float_as_uint(acc[i][j][8 * pq + 4 + k]), false, false);
-          e[k] = __uint_as_float(sw[0]);
-          e[4 + k] = __uint_as_float(sw[1]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] *= f[k];
-        if (o >= a.rows || m == 0) continue;
-        const int64_t at = o * a.width + d;
-        if (a.accumulate) {
-          float old[8];
-          if (m == 8) load8_any(dw, at, old);
-          else load_first(dw, at, m, old);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] += old[k];
-        }
-        if (m == 8) store8_any(dw, at, e);
-        else store_first(dw, at, m, e);
-      }
+      for (int k = 0; k < 8; ++k) e[k] += old[k];
     }
+    if (m == 8) store8_any(dw, at, e);
+    else store_first(dw, at, m, e);
+  }
 }
 
 // One 256 x 256 tile over one part of the tokens.
 template <typename WT>
 __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad(const WgradArgs a, int ni,
                                                                                              int no) {
-  __shared__ __attribute__((aligned(16))) char smem[kXSmem];
+  // the operands' stages; behind the loop half a tile's sums, in rows of 128 + 4
+  __shared__ __attribute__((aligned(16))) char smem[kXTile * 132 * 4];
   constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
   const int wave = threadIdx.x >> 6;
   const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
@@ -169,73 +172,15 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
         return t < full ? dz + t * ld : dzc + (t - full) * ld;
       },
       ld, ld - o0, acc);
-  put_tile<WT, MI, NI>(a, split, i0 + wm * WM, o0 + wn * WN, acc);
-}
-
-// Puts a wave's NI x NJ blocks at (di, dj) of the tile in LDS: rows of T + 4 values
-// along the width.
-template <int T, int NI, int NJ>
-__device__ __forceinline__ void stage_tile(float* tile, int di, int dj, const f32x16_t (&acc)[NI][NJ]) {
-  const int lane = threadIdx.x & 63, hi = lane >> 5;
+  // half of the width at a time through LDS
+  static_assert(WM == 128 && kXTile * (WM + 4) * 4 <= (int)sizeof(smem), "half a tile's sums fit");
+  float* const tile = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4_t*>(tile + (dj + 32 * j + (lane & 31)) * (T + 4) + di + 32 * i + 8 * q + 4 * hi) =
-            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-}
-
-// Stores a tile from LDS by whole rows (from the registers a store instruction would
-// reach 32 bytes of each of 32 rows).
-template <typename WT, int T>
-__device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t i0, int64_t o0, const float* tile) {
-  constexpr int C = T / 8, R = kDThreads / C;                 // chunks of a row, rows at a time
-  const int c = threadIdx.x % C * 8, r0 = threadIdx.x / C;
-  const int64_t d = i0 + c;
-  auto row = [&](int r, float (&e)[8]) {
-    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c);
-    const f32x4_t up = *reinterpret_cast<const f32x4_t*>(tile + r * (T + 4) + c + 4);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      e[k] = lo[k];
-      e[4 + k] = up[k];
-    }
-  };
-  float e[8];
-  if (a.splits > 1) {
-    float* const out = a.part + (int64_t)split * a.rows * a.ldp;
-    if (d >= a.ldp) return;
-#pragma unroll 2
-    for (int r = r0; r < T && o0 + r < a.rows; r += R) {
-      row(r, e);
-      store8(out, (o0 + r) * a.ldp + d, e);
-    }
-    return;
-  }
-  const int m = (int)min<int64_t>(a.width - d, 8);
-  if (m <= 0) return;
-  float f[8];
-  if (a.gain != nullptr) load_first(a.gain, d, m, f);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = a.gain != nullptr ? a.scale * f[k] : a.scale;
-  WT* const dw = static_cast<WT*>(a.dw);
-#pragma unroll 2
-  for (int r = r0; r < T && o0 + r < a.rows; r += R) {
-    const int64_t at = (o0 + r) * a.width + d;
-    row(r, e);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] *= f[k];
-    if (a.accumulate) {
-      float old[8];
-      if (m == 8) load8_any(dw, at, old);
-      else load_first(dw, at, m, old);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] += old[k];
-    }
-    if (m == 8) store8_any(dw, at, e);
-    else store_first(dw, at, m, e);
+  for (int h = 0; h < 2; ++h) {
+    __syncthreads();
+    if (wm == h) stage_tile<WM>(tile, 0, wn * WN, acc);
+    __syncthreads();
+    put_rows<WT, WM, kXTile, kXThreads>(a, split, i0 + h * WM, o0, tile);
   }
 }
 
@@ -456,7 +401,7 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     stage_tile<T>(tile, 32 * (wave >> 1), 32 * (wave & 1), mine);
   }
   __syncthreads();
-  put_rows<WT, T>(a, split, i0, o0, tile);
+  put_rows<WT, T, T, kDThreads>(a, split, i0, o0, tile);
 }
 
 // dw from the parts: 4 columns a thread, 8 parts in flight, added in their order.
