@@ -511,9 +511,10 @@ def profile_read():
 def __getattr__(name):
     # gradients.py and activations.py need torch at import, which nothing above does
     if name in ("clip_grads", "cross_entropy", "embedding", "embedding_grad", "grad_norm"):
-        from . import gradients
-        return getattr(gradients, name)
-    if name in ("Normed", "Packed", "mx_pack", "mx_unpack", "rms_norm", "rms_norm_grad", "weight_grad"):
-        from . import activations
-        return getattr(activations, name)
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import gradients as module
+    elif name in ("Normed", "Packed", "mx_pack", "mx_unpack", "rms_norm", "rms_norm_grad", "weight_grad"):
+        from . import activations as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = value = getattr(module, name)  # found without this function from now on (0.5 us a call)
+    return value
