@@ -482,8 +482,9 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
  *             (MUONH_PACK_NORMALIZED; what muonh_rms_norm_grad and, with the gain,
  *             muonh_weight_grad read) or y (MUONH_PACK_OUTPUT)
  *   n         0 .. 2^26;  width  1 .. 16384 (MUONH_ENOTIMPL above)
- * Squares are summed in fp64, the rest is fp32, each output rounded once.  Other
- * overlaps of an output with an input or an output are refused (MUONH_EINVAL).
+ * Squares are summed in fp64, the rest is fp32, each output rounded once; q's values
+ * are the e4m3 values nearest to the row in fp64.  Other overlaps of an output with an
+ * input or an output are refused (MUONH_EINVAL).
  */
 enum { MUONH_PACK_NORMALIZED = 0, MUONH_PACK_OUTPUT = 1 };
 int muonh_rms_norm(const void* x, int x_dtype, const void* residual, int h_dtype, const float* gain, float eps, int64_t n,

@@ -18,10 +18,28 @@ namespace muonh {
 namespace {
 
 // a^-1/2: the hardware's estimate and one Newton step, some 2^-50 off.
-__device__ __forceinline__ float rsqrt64(double a) {
+__device__ __forceinline__ double rsqrt64(double a) {
   const double r = __builtin_amdgcn_rsq(a);
   const double e = fma(-a * r, r, 1.0);
-  return a < (double)INFINITY ? (float)fma(0.5 * r, e, r) : a > 0.0 ? 0.f : (float)a;
+  return a < (double)INFINITY ? fma(0.5 * r, e, r) : a > 0.0 ? 0.0 : a;
+}
+
+// What becomes 8 bits is rounded to 4 significant ones.  Its fp32 value, a few roundings
+// off, decides as the exact one does unless it is within them of where two e4m3
+// values meet, whose last 19 bits are zeros: near_border tells (8 values: 1 wave in a
+// hundred), and such values are formed anew in fp64 and moved off the border to the
+// side where they lie.
+__device__ __forceinline__ bool near_border(const float (&v)[8]) {
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) low = min(low, (__float_as_uint(v[j]) + 4) & 0x7ffffu);
+  return low < 9;
+}
+__device__ __forceinline__ float settle(double t) {
+  const float f = (float)t;
+  uint32_t u = __float_as_uint(f);
+  if ((u & 0x7ffffu) == 0 && fabsf(f) < INFINITY && (double)f != t) u += fabs(t) > fabs((double)f) ? 1 : -1;
+  return __uint_as_float(u);
 }
 
 // TAIL: rows that do not end with a whole chunk of 8 (the others' code is free of the
@@ -92,7 +110,8 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
     }
     s = row_sum<NW>(s, red, turn);
     turn ^= 1;
-    const float rstd = rsqrt64(s / (double)width + a.eps);
+    const double rstd64 = rsqrt64(s / (double)width + a.eps);
+    const float rstd = (float)rstd64;
     if (lt == 0 && a.rstd != nullptr) gmem(a.rstd)[row] = rstd;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -100,10 +119,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
       const int m = c < nfull ? 8 : TAIL && c == nfull ? tail : 0;
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[k][j] *= rstd;
-        y[j] = v[k][j] * g[k][j];
-      }
+      for (int j = 0; j < 8; ++j) y[j] = v[k][j] * rstd * g[k][j];
       if (a.y != nullptr) {
         if (a.y_dt == DT_BF16) {
           bf16_t* const o = static_cast<bf16_t*>(a.y);
@@ -118,7 +134,17 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
       if (a.q != nullptr) {
         if (!a.packs_output) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = v[k][j];
+          for (int j = 0; j < 8; ++j) y[j] = v[k][j] * rstd;
+        }
+        if (near_border(y)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // copies that the compiler does not see through: it would keep fp64 values of the
+            // whole chunk in registers for this (90 and not 60: a norm of 268 MB 46 -> 56 us)
+            float h = v[k][j], f = a.packs_output ? g[k][j] : 1.f;
+            asm volatile("" : "+v"(h), "+v"(f));
+            y[j] = settle((double)h * rstd64 * (double)f);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = (TAIL ? j < m : m > 0) ? y[j] : 0.f;  // 0 times a NaN behind the row's end

@@ -225,6 +225,20 @@ def test_many_rows(n, d):
     assert bool(((dg.double() - prod.sum(0)).abs() <= (n / 256 + 80) * U * prod.abs().sum(0)).all())
 
 
+def test_smallest_eps_and_widths():
+    print("[case] norm, smallest eps", flush=True)
+    for width in (1, 8, 700):
+        x = torch.zeros(3, width)
+        x[1], x[2] = 1e-30, -5.0
+        r = mm.rms_norm(x.to(DEV), eps=1e-45, pack="output")
+        eps = float(torch.tensor(1e-45))
+        rstd = (x.double().square().mean(1) + eps) ** -0.5
+        within(r.rstd, rstd, rstd * U * 1.001, "rstd")
+        within(r.y, x.double() * rstd[:, None], (x.double() * rstd[:, None]).abs() * 3.01 * U, "y")
+        dx, _ = mm.rms_norm_grad(torch.zeros(3, width, device=DEV), r.packed, r.rstd)
+        assert bool((dx == 0).all())
+
+
 def test_empty_and_refused():
     print("[case] norm, empty and refused", flush=True)
     e = torch.zeros(0, 64, device=DEV, dtype=BF16)
@@ -254,3 +268,27 @@ def test_empty_and_refused():
                      ((x, p, rs), dict(out=x)), ((x.half(), p, rs), {})):
         with pytest.raises((ValueError, TypeError, mm.MuonhError)):
             mm.rms_norm_grad(*args, **kw)
+
+
+@pytest.mark.parametrize("pack", ["normalized", "output"])
+def test_packed_rows_are_rounded_once(pack):
+    """8-bit rows are those of the row in 64 bits: with some 10^7 values, whose fp32 value
+    lies on a border of e4m3 or on its other side ten times."""
+    print(f"[case] packed rows rounded once, {pack}", flush=True)
+    n, d = 10000, 1024
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    x = torch.randn(n, d, generator=g, device=DEV)
+    gain = torch.rand(d, generator=g, device=DEV) + 0.5
+    r = mm.rms_norm(x, gain, pack=pack, output=False)
+    v = x.double() * (x.double().square().mean(1, keepdim=True) + float(torch.tensor(1e-6))) ** -0.5
+    if pack == "output":
+        v = v * gain.double()
+    b = v.view(n, -1, 32)
+    m, e = torch.frexp(b.abs().amax(2, keepdim=True))
+    e = torch.where(m <= 0.875, e - 9, e - 8)
+    assert torch.equal((e[..., 0] + 127).to(torch.uint8), r.packed.scales.view(torch.uint8))
+    t = torch.ldexp(b, -e)
+    unit = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 3)
+    want = (torch.round(t / unit) * unit).view(n, d)
+    assert torch.equal(r.packed.q.double(), want)

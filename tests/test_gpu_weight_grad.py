@@ -69,6 +69,25 @@ def test_larger():
         check(mm.weight_grad(dz, p, gain=gain, out_dtype=F32), dz, p, gain)
 
 
+@pytest.mark.parametrize("n,rows,off", [(4100, 4093, 0), (4100, 4096, 1), (4096, 4096, 0)])
+def test_large_tiles_and_copies(n, rows, off):
+    """Sizes that 256 x 256 tiles take, with dz off the 16-byte grid (copied whole), and with
+    its last stage alone."""
+    print(f"[case] weight gradient, 256 tiles {n} {rows} {off}", flush=True)
+    width = 4096
+    dz, p, gain = inputs(n, rows, width)
+    z = torch.zeros(n * rows + 8, dtype=BF16, device=DEV)
+    z[off:off + n * rows] = dz.view(-1)
+    dz = z[off:off + n * rows].view(n, rows)
+    size = mm.load().muonh_weight_grad_workspace(dz.data_ptr(), n, rows, width)
+    copied = n if rows % 8 or off else n % 64
+    assert 2 * width * n + 2 * copied * rows <= size <= 2 * width * (n + 192) + 2 * (copied + 64) * (rows + 8) + 1024
+    check(mm.weight_grad(dz, p, gain=gain, out_dtype=F32), dz, p, gain)
+    base = torch.randn(rows, width, device=DEV).bfloat16()
+    acc = base.clone()
+    check(mm.weight_grad(dz, p, out=acc, accumulate=True, scale=-2.0), dz, p, None, -2.0, base)
+
+
 def test_of_the_norm():
     """From what the norm kept: the gradient behind its output."""
     print("[case] weight gradient behind the norm", flush=True)
