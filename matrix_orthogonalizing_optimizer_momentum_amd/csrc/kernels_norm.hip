@@ -7,7 +7,7 @@
 // it is written.  The row in 8 bits (mx.h) leaves in the same pass, so that
 // the backward pass reads 1.03 bytes a value instead of h and y.
 //
-// A row belongs to 1 to 16 waves by its length (norm_shape), a lane to the same
+// A row belongs to 8 to 1024 threads by its length (norm_shape), a thread to the same
 // columns of every row of its workgroup, in chunks of 8.  Squares are summed in
 // fp64: h^2 may leave fp32's range, and the sum's rounding would reach every value
 // of the row.
@@ -44,11 +44,11 @@ __device__ __forceinline__ float settle(double t) {
 
 // TAIL: rows that do not end with a whole chunk of 8 (the others' code is free of the
 // values taken one by one).  ONCE: past the caches.
-template <typename XT, typename RT, bool RES, bool TAIL, bool ONCE, int NW, int CH>
-__global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a) {
-  constexpr int G = norm_threads(NW) / (64 * NW);  // rows at a time
-  __shared__ double red[2][NW];
-  const int lt = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
+template <typename XT, typename RT, bool RES, bool TAIL, bool ONCE, int L, int CH>
+__global__ __launch_bounds__(norm_threads(L)) void k_rms_norm(const NormArgs a) {
+  constexpr int G = norm_threads(L) / L;  // rows at a time
+  __shared__ double red[2][row_waves(L)];
+  const int lt = L <= 64 ? threadIdx.x & (L - 1) : threadIdx.x;
   const int64_t width = a.width, nblk = mx_blocks(width);
   const int nfull = (int)(width / 8), tail = (int)(width % 8);
   const XT* const x = static_cast<const XT*>(a.x);
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
   float g[CH][8];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = lt + 64 * NW * k;
+    const int c = lt + L * k;
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[k][j] = 1.f;
     if (a.gain != nullptr) {
@@ -65,13 +65,13 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
     }
   }
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * G + (G == 1 ? 0 : threadIdx.x >> 6); row < a.n; row += (int64_t)gridDim.x * G) {
+  for (int64_t row = (int64_t)blockIdx.x * G + (G == 1 ? 0 : threadIdx.x / L); row < a.n; row += (int64_t)gridDim.x * G) {
     const int64_t at = row * width;
     Raw8<XT> rx[CH];
     Raw8<RT> rr[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       if (c < nfull) {
         load_chunk<ONCE>(rx[k], x, at + 8 * c);
         if constexpr (RES) load_chunk<ONCE>(rr[k], res, at + 8 * c);
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
     double s = 0.0;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       if (c < nfull) {
         rx[k].unpack(v[k]);
         if constexpr (RES) {
@@ -108,14 +108,14 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s = fma((double)v[k][j], (double)v[k][j], s);
     }
-    s = row_sum<NW>(s, red, turn);
+    s = row_sum<L>(s, red, turn);
     turn ^= 1;
     const double rstd64 = rsqrt64(s / (double)width + a.eps);
     const float rstd = (float)rstd64;
     if (lt == 0 && a.rstd != nullptr) gmem(a.rstd)[row] = rstd;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       const int m = c < nfull ? 8 : TAIL && c == nfull ? tail : 0;
       float y[8];
 #pragma unroll
@@ -161,10 +161,10 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm(const NormArgs a)
 template <typename XT, typename RT, bool RES>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
   const int64_t each = sizeof(XT) + (RES ? 2 * sizeof(RT) : 0) + (a.y ? (a.y_dt == DT_BF16 ? 2 : 4) : 0) + (a.q ? 1 : 0);
-  return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto nw, auto ch) {
-    constexpr int NW = decltype(nw)::value, CH = decltype(ch)::value, NT = norm_threads(NW), G = NT / (64 * NW);
+  return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto lanes, auto ch) {
+    constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, NT = norm_threads(L), G = NT / L;
     const int64_t blocks = std::min<int64_t>((a.n + G - 1) / G, 2048);
-    k_rms_norm<XT, RT, RES, decltype(tail)::value, decltype(once)::value, NW, CH><<<dim3((uint32_t)blocks), NT, 0, s>>>(a);
+    k_rms_norm<XT, RT, RES, decltype(tail)::value, decltype(once)::value, L, CH><<<dim3((uint32_t)blocks), NT, 0, s>>>(a);
     return hipGetLastError();
   });
 }

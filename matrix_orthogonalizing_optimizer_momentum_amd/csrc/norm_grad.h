@@ -84,18 +84,18 @@ __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int block) {
 // RT: type of dx, dres and x (x: the norm's input; PACKED: xn in 8 bits instead).
 // COLS: workgroups behind the first `blocks` sum the gain's gradient by columns
 // (an instance of its own: the others need fewer registers).
-template <typename YT, typename RT, bool PACKED, bool TAIL, bool ONCE, bool COLS, int NW, int CH>
-__global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGradArgs a, int blocks) {
-  constexpr int NT = norm_threads(NW), G = NT / (64 * NW);
+template <typename YT, typename RT, bool PACKED, bool TAIL, bool ONCE, bool COLS, int L, int CH>
+__global__ __launch_bounds__(norm_threads(L)) void k_rms_norm_grad(const NormGradArgs a, int blocks) {
+  constexpr int NT = norm_threads(L), G = NT / L;
   if constexpr (COLS) {
     if ((int)blockIdx.x >= blocks) {
       gain_columns<YT, RT, PACKED, NT>(a, (int)blockIdx.x - blocks);
       return;
     }
   }
-  __shared__ float red[2][NW];
-  __shared__ float lsum[G == 1 || COLS ? 1 : (G - 1) * 64 * CH * 8];
-  const int lt = NW == 1 ? threadIdx.x & 63 : threadIdx.x, grp = NW == 1 ? threadIdx.x >> 6 : 0;
+  __shared__ float red[2][row_waves(L)];
+  __shared__ float lsum[G == 1 || COLS ? 1 : (G - 1) * L * CH * 8];
+  const int lt = L <= 64 ? threadIdx.x & (L - 1) : threadIdx.x, grp = G == 1 ? 0 : threadIdx.x / L;
   const int64_t width = a.width, nblk = mx_blocks(width);
   const int nfull = (int)(width / 8), tail = (int)(width % 8);
   const YT* const dy = static_cast<const YT*>(a.dy);
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
   const RT* const dres = static_cast<const RT*>(a.dres);
   float g[CH][8], acc[CH][8];
   auto load_gain = [&](int k) {
-    const int c = lt + 64 * NW * k;
+    const int c = lt + L * k;
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[k][j] = 1.f;
     if (a.gain != nullptr) {
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
     uint32_t rs[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       if (c < nfull) {
         load_chunk<ONCE>(ry[k], dy, at + 8 * c);
         if constexpr (PACKED) {
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       const int m = TAIL && c == nfull ? tail : 0;
       if (!TAIL || c < nfull) ry[k].unpack(u[k]);
       else load_first(dy, at + 8 * (int64_t)c, m, u[k]);
@@ -165,11 +165,11 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
         s = fmaf(u[k][j], xn[k][j], s);
       }
     }
-    s = row_sum<NW>(s, red, turn) * inv;
+    s = row_sum<L>(s, red, turn) * inv;
     turn ^= 1;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = lt + 64 * NW * k;
+      const int c = lt + L * k;
       const int m = c < nfull ? 8 : TAIL && c == nfull ? tail : 0;
       float d[8];
 #pragma unroll
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
     for (int k = 0; k < CH; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (grp > 0) lsum[(((grp - 1) * CH + k) * 8 + j) * 64 + lt] = acc[k][j];
+        if (grp > 0) lsum[(((grp - 1) * CH + k) * 8 + j) * L + lt] = acc[k][j];
     __syncthreads();
     if (grp > 0) return;
 #pragma unroll
@@ -198,11 +198,11 @@ __global__ __launch_bounds__(norm_threads(NW)) void k_rms_norm_grad(const NormGr
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[k][j] += lsum[((w * CH + k) * 8 + j) * 64 + lt];
+        for (int j = 0; j < 8; ++j) acc[k][j] += lsum[((w * CH + k) * 8 + j) * L + lt];
   }
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = lt + 64 * NW * k;
+    const int c = lt + L * k;
     const int64_t at = (int64_t)blockIdx.x * width + 8 * (int64_t)c;
     if (c < nfull) store8_any(a.part, at, acc[k]);
     else if (TAIL && c == nfull) store_first(a.part, at, tail, acc[k]);
@@ -214,13 +214,13 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
   const int blocks = norm_grad_blocks(a.n, a.width);
   const bool columns = a.dgain != nullptr && a.part == nullptr;
   const int64_t each = sizeof(YT) + (a.dres ? 2 : 1) * sizeof(RT) + (PACKED ? 1 : sizeof(RT));
-  return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto nw, auto ch) {
-    constexpr int NW = decltype(nw)::value, CH = decltype(ch)::value, NT = norm_threads(NW);
+  return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto lanes, auto ch) {
+    constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, NT = norm_threads(L);
     if (columns) {
       const int64_t sums = (a.width + 31) / 32;
-      k_rms_norm_grad<YT, RT, PACKED, true, false, true, NW, CH><<<dim3((uint32_t)(blocks + sums)), NT, 0, s>>>(a, blocks);
+      k_rms_norm_grad<YT, RT, PACKED, true, false, true, L, CH><<<dim3((uint32_t)(blocks + sums)), NT, 0, s>>>(a, blocks);
     } else {
-      k_rms_norm_grad<YT, RT, PACKED, decltype(tail)::value, decltype(once)::value, false, NW, CH>
+      k_rms_norm_grad<YT, RT, PACKED, decltype(tail)::value, decltype(once)::value, false, L, CH>
           <<<dim3(blocks), NT, 0, s>>>(a, blocks);
     }
     return hipGetLastError();

@@ -292,3 +292,32 @@ def test_packed_rows_are_rounded_once(pack):
     unit = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 3)
     want = (torch.round(t / unit) * unit).view(n, d)
     assert torch.equal(r.packed.q.double(), want)
+
+
+@pytest.mark.parametrize("n,d", [(5001, 8), (4999, 50), (30000, 64), (7000, 65), (3001, 100), (50001, 128), (2500, 175), (2049, 256),
+                                 (1500, 257)])
+def test_narrow_rows(n, d):
+    """Rows that share a wave (heads of an attention), in every direction."""
+    print(f"[case] narrow rows {n} {d}", flush=True)
+    test_many_rows(n, d)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(n)
+    x = torch.randn(n, d, generator=g, device=DEV)
+    gain = torch.rand(d, generator=g, device=DEV) + 0.5
+    # each row by itself, whatever its neighbours in the wave hold
+    r = mm.rms_norm(x, gain, pack="normalized")
+    y = x.clone()
+    y[1::3] = math.nan
+    s = mm.rms_norm(y, gain, pack="normalized")
+    keep = [k for k in range(n) if k % 3 != 1]
+    assert torch.equal(s.y[keep], r.y[keep]) and torch.equal(s.rstd[keep], r.rstd[keep])
+    assert torch.equal(s.packed.q.view(torch.uint8)[keep], r.packed.q.view(torch.uint8)[keep])
+    assert bool(s.y[1::3].isnan().all())
+    for kept in (r.packed, x):
+        dx, dg = mm.rms_norm_grad(x, kept, r.rstd, gain)
+        xn = mm.mx_unpack(kept, out_dtype=F32).double() if kept is not x else x.double() * r.rstd.double()[:, None]
+        prod = x.double() * xn
+        assert bool(((dg.double() - prod.sum(0)).abs() <= (n / 256 + 80) * U * prod.abs().sum(0)).all())
+        few, dg2 = mm.rms_norm_grad(x[:300], kept[:300] if kept is x else type(kept)(kept.q[:300], kept.scales[:300]), r.rstd[:300], gain)
+        assert torch.equal(few, dx[:300])
+        assert bool(((dg2.double() - prod[:300].sum(0)).abs() <= 340 * U * prod[:300].abs().sum(0)).all())
