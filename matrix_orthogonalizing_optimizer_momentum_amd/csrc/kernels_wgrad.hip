@@ -5,7 +5,9 @@
 // Both operands lie along their columns, the sum runs over the tokens.  x is
 // brought to bf16 along the tokens once (exact: e4m3 times a power of two), a
 // pass of 3 bytes a value beside the product's 2 rows flop; dz is read as it is
-// through the transposing LDS read of the main loop (product.h), sums in fp32.
+// through the transposing LDS read of the main loop (product.h), or brought along the
+// tokens too where x is so wide that the plain reads are worth a pass (api_act.hip);
+// sums in fp32.
 // The gain is a factor of the result's columns.  Weights of few tiles have their
 // tokens cut into parts, one product each, that a second launch adds in order.
 #include <algorithm>
@@ -19,61 +21,105 @@ namespace muonh {
 
 namespace {
 
-// 64 tokens x 64 columns of q a workgroup (x < xtiles), transposed; behind them
-// 64 rows x 256 columns of dz's copy.
-__global__ __launch_bounds__(256) void k_wgrad_prepare(const WgradArgs a, int xtiles, int xcols, int dcols) {
-  __shared__ uint16_t t[64][72];
-  if ((int)blockIdx.x < xtiles) {
-    const int64_t r0 = (int64_t)(blockIdx.x / xcols) * 64, c0 = (int64_t)(blockIdx.x % xcols) * 64;
-    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
-    const int64_t nblk = mx_blocks(a.width);
-    const int m = (int)min<int64_t>(max<int64_t>(a.width - c0 - c, 0), 8);
+// 8 tokens of 8 columns (16 bits each) to 8 runs of 8 tokens.
+__device__ __forceinline__ void turn(const u32x4_t (&w)[8], u32x4_t (&run)[8]) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t row = r0 + r + 32 * k;
-      float v[8];
+  for (int h = 0; h < 4; ++h)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      if (row < a.n && m > 0) {
-        const uint8_t* const p = a.q + row * a.width + c0 + c;
-        const float f = mx_factor(gmem(a.scales)[row * nblk + (c0 + c) / kMxBlock]);
-        from_e4m3(m == 8 ? load_q8(p) : load_q8(p, m), f, v);
+    for (int p = 0; p < 4; ++p) {
+      run[2 * h][p] = __builtin_amdgcn_perm(w[2 * p + 1][h], w[2 * p][h], 0x05040100);
+      run[2 * h + 1][p] = __builtin_amdgcn_perm(w[2 * p + 1][h], w[2 * p][h], 0x07060302);
+    }
+}
+
+// 128 tokens x 128 columns along the tokens, zeros behind the last one: x (X), or dz.
+// A thread turns 8 x 8 values in registers; LDS brings the runs of a column together
+// (16 bytes of chunk c of row r at c ^ swizzle), so that whole lines are read and stored.
+template <bool X>
+__device__ __forceinline__ void turn_tile(const WgradArgs& a, int64_t t0, int64_t c0, uint16_t (*lds)[128]) {
+  const int cg = threadIdx.x & 15, og = threadIdx.x >> 4;
+  const int64_t width = X ? a.width : a.rows, c = c0 + 8 * cg, nblk = mx_blocks(a.width);
+  const int m = (int)min<int64_t>(max<int64_t>(width - c, 0), 8);
+  u32x4_t w[8];
+  uint32_t f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t t = t0 + 8 * og + k;
+    w[k] = u32x4_t{0u, 0u, 0u, 0u};
+    f[k] = 127;
+    if (t < a.n && m > 0) {
+      if constexpr (X) {
+        const uint8_t* const p = a.q + t * width + c;
+        f[k] = gmem(a.scales)[t * nblk + c / kMxBlock];
+        const u32x2_t q = m == 8 ? load_q8(p) : load_q8(p, m);
+        w[k][0] = q[0];
+        w[k][1] = q[1];
+      } else {
+        const uint16_t* const p = a.dz + t * width + c;
+        if (m == 8) {
+          w[k] = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < m) w[k][j / 2] |= (uint32_t)gmem(p)[j] << (16 * (j & 1));
+        }
       }
-      u32x4_t w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      *reinterpret_cast<u32x4_t*>(&t[r + 32 * k][c]) = w;
     }
-    __syncthreads();
+  }
+  if constexpr (X) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      u32x4_t w;
+    for (int k = 0; k < 8; ++k) w[k] = e4m3_to_bf16(u32x2_t{w[k][0], w[k][1]}, f[k]);
+  }
+  u32x4_t run[8];
+  turn(w, run);
+  // rows 8 apart are written at once, consecutive chunks of a row are read
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = (uint32_t)t[c + 2 * e][r + 32 * k] | (uint32_t)t[c + 2 * e + 1][r + 32 * k] << 16;
-      *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(a.xt + (c0 + r + 32 * k) * a.ldxt + r0 + c)) = w;
-    }
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4_t*>(&lds[8 * cg + j][(og ^ cg) * 8]) = run[j];
+  __syncthreads();
+  uint16_t* const out = X ? a.xt : a.dzt;
+  const int64_t rows = min<int64_t>((width + 7) / 8 * 8 - c0, 128);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = (threadIdx.x >> 4) + 16 * k, o = threadIdx.x & 15;
+    if (r < rows)
+      *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(out + (c0 + r) * a.ldxt + t0 + 8 * o)) =
+          *reinterpret_cast<const u32x4_t*>(&lds[r][(o ^ (r >> 3)) * 8]);
+  }
+}
+
+// What a product of 256 tiles reads: x along the tokens (workgroups below xtiles), and
+// dz along them too (TURN), or dz's last, partial stage or all of it as it lies, padded with
+// zeros.
+template <bool TURN>
+__global__ __launch_bounds__(256) void k_wgrad_prepare(const WgradArgs a, int xtiles, int xcols, int dcols) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[128][128];
+  if ((int)blockIdx.x < xtiles) {
+    turn_tile<true>(a, (int64_t)(blockIdx.x / xcols) * 128, (int64_t)(blockIdx.x % xcols) * 128, lds);
     return;
   }
   const int b = (int)blockIdx.x - xtiles;
-  const int64_t r0 = a.dfull + (int64_t)(b / dcols) * 64, c = (int64_t)(b % dcols) * 256 + (threadIdx.x & 31) * 8;
-  if (c >= a.lddz) return;
-  const int m = (int)min<int64_t>(max<int64_t>(a.rows - c, 0), 8);
+  if constexpr (TURN) {
+    turn_tile<false>(a, (int64_t)(b / dcols) * 128, (int64_t)(b % dcols) * 128, lds);
+  } else {
+    const int64_t r0 = a.dfull + (int64_t)(b / dcols) * 64, c = (int64_t)(b % dcols) * 256 + (threadIdx.x & 31) * 8;
+    if (c >= a.lddz) return;
+    const int m = (int)min<int64_t>(max<int64_t>(a.rows - c, 0), 8);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t row = r0 + (threadIdx.x >> 5) + 8 * k;
-    u32x4_t w = {0u, 0u, 0u, 0u};
-    if (row < a.n) {
-      const uint16_t* const p = a.dz + row * a.rows + c;
-      if (m == 8) {
-        w = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p));
-      } else {
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = r0 + (threadIdx.x >> 5) + 8 * k;
+      u32x4_t w = {0u, 0u, 0u, 0u};
+      if (row < a.n) {
+        const uint16_t* const p = a.dz + row * a.rows + c;
+        if (m == 8) {
+          w = *reinterpret_cast<const MUONH_GLOBAL u32x4_u*>(gmem(p));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < m) w[j / 2] |= (uint32_t)gmem(p)[j] << (16 * (j & 1));
+          for (int j = 0; j < 8; ++j)
+            if (j < m) w[j / 2] |= (uint32_t)gmem(p)[j] << (16 * (j & 1));
+        }
       }
+      *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(a.dzt + (row - a.dfull) * a.lddz + c)) = w;
     }
-    *reinterpret_cast<MUONH_GLOBAL u32x4_t*>(gmem(a.dzc + (row - a.dfull) * a.lddz + c)) = w;
   }
 }
 
@@ -147,7 +193,7 @@ __device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t 
 }
 
 // One 256 x 256 tile over one part of the tokens.
-template <typename WT>
+template <typename WT, bool TURN>
 __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad(const WgradArgs a, int ni,
                                                                                              int no) {
   // the operands' stages; behind the loop half a tile's sums, in rows of 128 + 4
@@ -162,16 +208,23 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   const int all = (int)(a.npad / kXStage);
   const int64_t s0 = (uint32_t)(all * split) / (uint32_t)a.splits, s1 = (uint32_t)(all * (split + 1)) / (uint32_t)a.splits;
   const uint16_t* const xt = a.xt + i0 * a.ldxt + s0 * kXStage;
-  const uint16_t *const dz = a.dz + o0, *const dzc = a.dzc + o0;
-  const int64_t full = a.dfull, ld = a.lddz;
   f32x16_t acc[MI][NI];
-  product<false, true, MI, NI>(
-      smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
-      [=](int s) {
-        const int64_t t = (s0 + s) * kXStage;
-        return t < full ? dz + t * ld : dzc + (t - full) * ld;
-      },
-      ld, ld - o0, acc);
+  if constexpr (TURN) {
+    const uint16_t* const dzt = a.dzt + o0 * a.ldxt + s0 * kXStage;
+    product<false, false, MI, NI>(
+        smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
+        [=](int s) { return dzt + (int64_t)s * kXStage; }, a.ldxt, 0, acc);
+  } else {
+    const uint16_t *const dz = a.dz + o0, *const dzc = a.dzt + o0;
+    const int64_t full = a.dfull, ld = a.lddz;
+    product<false, true, MI, NI>(
+        smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
+        [=](int s) {
+          const int64_t t = (s0 + s) * kXStage;
+          return t < full ? dz + t * ld : dzc + (t - full) * ld;
+        },
+        ld, ld - o0, acc);
+  }
   // half of the width at a time through LDS
   static_assert(WM == 128 && kXTile * (WM + 4) * 4 <= (int)sizeof(smem), "half a tile's sums fit");
   float* const tile = reinterpret_cast<float*>(smem);
@@ -450,10 +503,13 @@ __global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a) {
 }  // namespace
 
 hipError_t launch_wgrad_prepare(const WgradArgs& a, hipStream_t s) {
-  const int64_t xcols = (a.width + 63) / 64, xtiles = a.npad / 64 * xcols;
-  const int64_t dcols = (a.lddz + 255) / 256, dtiles = (a.npad - a.dfull) / 64 * dcols;
+  const int64_t ttiles = (a.n + 127) / 128, xcols = (a.width + 127) / 128, xtiles = ttiles * xcols;
+  const int64_t dcols = a.turn ? (a.rows + 127) / 128 : (a.lddz + 255) / 256;
+  const int64_t dtiles = a.turn ? ttiles * dcols : (a.npad - a.dfull) / 64 * dcols;
   if (xtiles + dtiles == 0) return hipSuccess;
-  k_wgrad_prepare<<<dim3((uint32_t)(xtiles + dtiles)), 256, 0, s>>>(a, (int)xtiles, (int)xcols, (int)dcols);
+  const dim3 g((uint32_t)(xtiles + dtiles));
+  if (a.turn) k_wgrad_prepare<true><<<g, 256, 0, s>>>(a, (int)xtiles, (int)xcols, (int)dcols);
+  else k_wgrad_prepare<false><<<g, 256, 0, s>>>(a, (int)xtiles, (int)xcols, (int)dcols);
   return hipGetLastError();
 }
 
@@ -462,7 +518,8 @@ template <typename WT>
 hipError_t wgrad(const WgradArgs& a, hipStream_t s) {
   const int ni = (int)((a.width + a.tile - 1) / a.tile), no = (int)((a.rows + a.tile - 1) / a.tile);
   const dim3 g((uint32_t)((int64_t)ni * no * a.splits));
-  if (a.tile == kXTile) k_wgrad<WT><<<g, kXThreads, 0, s>>>(a, ni, no);
+  if (a.tile == kXTile && a.turn) k_wgrad<WT, true><<<g, kXThreads, 0, s>>>(a, ni, no);
+  else if (a.tile == kXTile) k_wgrad<WT, false><<<g, kXThreads, 0, s>>>(a, ni, no);
   else if (a.tile == 128) k_wgrad_direct<WT, 128><<<g, kDThreads, 0, s>>>(a, ni, no);
   else k_wgrad_direct<WT, 64><<<g, kDThreads, 0, s>>>(a, ni, no);
   const hipError_t e = hipGetLastError();

@@ -17,12 +17,13 @@ struct WgradArgs {
   const float* gain;                 // width, or nullptr
   void* dw;                          // rows x width
   uint16_t* xt;                      // width up to a tile rows of ldxt: q's values in bf16 along the tokens
-  uint16_t* dzc;                     // dz's rows [dfull, n), padded with zeros to a whole stage, of lddz
+  uint16_t* dzt;                     // turn: dz along the tokens, rows up to a tile of ldxt; else dz's rows [dfull, n),
+                                     // padded with zeros to a whole stage, of lddz
   float* part;                       // [splits][rows][ldp], with splits > 1
   int64_t n, npad, rows, width, ldxt, lddz, dfull, ldp;
   int64_t whole;                     // stages that the 64 and 128 tiles read whole, over the rows' ends
   float scale;
-  int32_t dw_dt, accumulate, splits, tile;  // tile: 256 (from xt and dzc), or 128 or 64 from q and dz
+  int32_t dw_dt, accumulate, splits, turn, tile;  // tile: 256 (from xt and dz or dzt), or 128 or 64 from q and dz
 };
 
 hipError_t launch_wgrad_prepare(const WgradArgs& a, hipStream_t s);

@@ -88,6 +88,22 @@ def test_large_tiles_and_copies(n, rows, off):
     check(mm.weight_grad(dz, p, out=acc, accumulate=True, scale=-2.0), dz, p, None, -2.0, base)
 
 
+@pytest.mark.parametrize("n,rows,width,off", [(2100, 4096, 8192, 0), (2049, 4001, 8192, 0), (2176, 4041, 16377, 1)])
+def test_wide(n, rows, width, off):
+    """Sizes whose dz is brought along the tokens as well."""
+    print(f"[case] weight gradient, wide {n} {rows} {width} {off}", flush=True)
+    dz, p, gain = inputs(n, rows, width)
+    z = torch.zeros(n * rows + 8, dtype=BF16, device=DEV)
+    z[off:off + n * rows] = dz.view(-1)
+    dz = z[off:off + n * rows].view(n, rows)
+    size = mm.load().muonh_weight_grad_workspace(dz.data_ptr(), n, rows, width)
+    assert size >= 2 * n * (rows + width)
+    check(mm.weight_grad(dz, p, gain=gain, out_dtype=F32), dz, p, gain)
+    base = torch.randn(rows, width, device=DEV).bfloat16()
+    acc = base.clone()
+    check(mm.weight_grad(dz, p, out=acc, accumulate=True, scale=-2.0), dz, p, None, -2.0, base)
+
+
 def test_of_the_norm():
     """From what the norm kept: the gradient behind its output."""
     print("[case] weight gradient behind the norm", flush=True)
