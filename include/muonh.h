@@ -517,7 +517,7 @@ int muonh_rms_norm_grad(const void* dy, int dy_dtype, const void* x, const void*
 /*
  * muonh_mx_pack, muonh_mx_unpack -- a matrix to 8 bits, and back (rounded once to
  * out_dtype).  x, out: MUONH_F32 or MUONH_BF16, n x width; n 0 .. 2^26, width
- * 1 .. 2^20.
+ * 1 .. 2^20, together up to 2^40 values (MUONH_ENOTIMPL above).
  */
 int muonh_mx_pack(const void* x, int x_dtype, int64_t n, int64_t width, void* q, void* scales, void* stream);
 int muonh_mx_unpack(const void* q, const void* scales, int64_t n, int64_t width, void* out, int out_dtype, void* stream);
@@ -536,9 +536,10 @@ int muonh_mx_unpack(const void* q, const void* scales, int64_t n, int64_t width,
  *             accumulate = 1 adds to it; must not overlap the inputs
  *   n         0 .. 2^22;  rows, width  1 .. 2^20, together up to 2^37 values of dw
  *             and 2^35 of dz or x (MUONH_ENOTIMPL above); n = 0 clears dw (or leaves it)
- * Sums are fp32, rounded once.  Rows of dz that are not a multiple of 8 values, or
- * not on a 16-byte grid, are copied to the workspace once; of dz only its address
- * matters to muonh_weight_grad_workspace.
+ * Sums are fp32, rounded once.  Large products keep x in bf16 in the workspace, parts
+ * of the sums, and dz where its rows are not a multiple of 8 values or not on a 16-byte
+ * grid, or width is 8192 or more; of dz only its address matters to
+ * muonh_weight_grad_workspace.
  */
 size_t muonh_weight_grad_workspace(const void* dz, int64_t n, int64_t rows, int64_t width);
 int muonh_weight_grad(const void* dz, const void* q, const void* scales, const float* gain, float scale, int64_t n,

@@ -3,8 +3,9 @@
 //
 // A call of one token runs for some 4 us; the same checks and allocations made
 // from Python take 6 to 14 us before it starts (a norm with its residual 13.4 us a
-// call there, 7.0 here, of which the launch takes 4).  The entry points are handed over as addresses
-// (bind), so this extension and libmuonh.so are built without each other.
+// call there, 6.6 here, of which the launch takes 4).  The entry points are handed
+// over as addresses (bind), so this extension and libmuonh.so are built without each
+// other.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

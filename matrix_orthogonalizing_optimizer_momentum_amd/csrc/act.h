@@ -13,7 +13,7 @@ namespace muonh {
 constexpr int64_t kMxBlock = 32;
 __host__ __device__ inline int64_t mx_blocks(int64_t width) { return (width + kMxBlock - 1) / kMxBlock; }
 
-// A row is held in registers: at most 16 waves of 2 chunks of 8 values a lane.
+// A row is held in registers: at most 1024 threads of 2 chunks of 8 values.
 constexpr int64_t kNormMaxWidth = 16384, kActMaxTokens = (int64_t)1 << 26, kActMaxWidth = (int64_t)1 << 20;
 
 // What moves more bytes than this is read and written past the caches, as no cache
@@ -60,12 +60,12 @@ struct MxArgs {
 };
 
 // Workgroups of the norm's gradient, and so partial sums of the gain's (8192 x 2048:
-// 256 take 41.9 us, 512 28.0, 768 25.3, 1536 31.0; 8192 x 8192, 16 waves a row: 256
-// 90.7, 512 93.0).
+// 256 take 41.9 us, 512 28.0, 768 25.3, 1536 31.0; 8192 x 8192, 1024 threads a
+// row: 256 90.7, 512 93.0).
 int norm_grad_blocks(int64_t n, int64_t width);
 // Rows few enough to be read again by columns in the same launch, which the host
 // takes 6 us for, two 10 (on the GPU 64 x 2048 4.5 us against 5.5, 512 x 2048 8.4 and 8.3,
-// 777 x 1999 17.0 and 13.1).
+// 777 x 1999 17.0 and 11.6).
 inline bool norm_grad_columns(int64_t n, int64_t width) { return n <= 512 && n * width <= (int64_t)3 << 19; }
 
 hipError_t launch_rms_norm(int x_dt, int res_dt, const NormArgs& a, hipStream_t s);  // res_dt: -1 without res

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(1024) void k_norm_gain_sum(const float* __restrict_
 }  // namespace
 
 // Some 4 rows each in turn, at least a workgroup a compute unit, at most what runs at once
-// (768 x 1999 and 2000 x 768 fp32: 256 and 512 workgroups 12.7 and 10.2 us, 768 15.2 and 10.9).
+// (777 x 1999 and 2000 x 768 fp32: 256 and 512 workgroups 12.7 and 10.2 us, 768 15.2 and 10.9).
 int norm_grad_blocks(int64_t n, int64_t width) {
   const int l = norm_shape(width).lanes;
   const int64_t rows = std::max<int64_t>(1, (n + norm_threads(l) / l - 1) / (norm_threads(l) / l));

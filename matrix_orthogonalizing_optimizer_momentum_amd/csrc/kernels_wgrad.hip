@@ -242,13 +242,14 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
 // alignment; x is brought to bf16 there) into LDS as it lies, tokens down, and
 // both operands are read transposed.  Rows are padded by 64 bytes, so that the 4
 // tokens which a transposing read touches lie in different banks.  Those reads (64
-// bytes a clock) bound the loop, so a wave multiplies 64 x 64: a quarter of a tile
-// of 128, or a whole tile of 64 for a quarter of the tokens, with the waves' sums
-// joined at the end.  Two stages are
+// bytes a clock) take the most of a 128 tile's stage, 64 KB or some 0.45 of its 0.7 us, so
+// a wave multiplies 64 x 64: a quarter of a tile of 128, or a whole tile of 64 for a
+// quarter of the tokens, with the waves' sums joined at the end.  Two stages are
 // in flight in registers and one in LDS beside the one that is multiplied, with
-// one barrier a stage.  What lies behind a row's end is read as it comes (the next
-// row) and reaches only results that are not kept; stages whose reads would
-// leave a buffer are read value by value, with zeros behind the last token.
+// one barrier a stage (four in flight, or the stores between the products, took
+// as long).  What lies behind a row's end is read as it comes (the next row) and
+// reaches only results that are not kept; stages whose reads would leave a buffer
+// are read value by value, with zeros behind the last token.
 template <typename WT, int T>
 __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad_direct(const WgradArgs a, int ni,
                                                                                                     int no) {

@@ -1,4 +1,4 @@
-// What the norm's kernels share: sums over a row's waves, and which waves those are.
+// What the norm's kernels share: sums over a row's threads, and which threads those are.
 #pragma once
 #include <algorithm>
 #include <type_traits>
