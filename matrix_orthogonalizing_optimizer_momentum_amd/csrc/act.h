@@ -64,8 +64,8 @@ struct MxArgs {
 // row: 256 90.7, 512 93.0).
 int norm_grad_blocks(int64_t n, int64_t width);
 // Rows few enough to be read again by columns in the same launch, which the host
-// takes 6 us for, two 10 (on the GPU 64 x 2048 4.5 us against 5.5, 512 x 2048 8.4 and 8.3,
-// 777 x 1999 17.0 and 11.6).
+// takes 6 us for, two 10 (on the GPU 64 x 2048 4.5 us against 5.5, 512 x 2048 8.2 and 7.2,
+// 777 x 1999 fp32 15.0 and 12.8).
 inline bool norm_grad_columns(int64_t n, int64_t width) { return n <= 512 && n * width <= (int64_t)3 << 19; }
 
 hipError_t launch_rms_norm(int x_dt, int res_dt, const NormArgs& a, hipStream_t s);  // res_dt: -1 without res

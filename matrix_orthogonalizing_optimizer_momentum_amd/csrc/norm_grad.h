@@ -17,18 +17,24 @@
 namespace muonh {
 namespace {
 
-// The gain's gradient of 32 columns over all rows, by one workgroup: 4 lanes along
-// a row, the others down the rows.
-template <typename YT, typename RT, bool PACKED, int NT>
+// Lanes along a row below, for rows of l threads: 4, and 2 where 32 columns a workgroup
+// would leave few workgroups (2 lanes against 4: 512 x 768 5.8 us and 7.9, 256 x 2048 5.7
+// and 5.2, 512 x 4096 11.0 and 9.1).
+constexpr int gain_lanes(int l) { return l <= 128 ? 2 : 4; }
+
+// The gain's gradient of 8 columns a lane over all rows, by one workgroup: GL lanes
+// along a row, the others down the rows.
+template <typename YT, typename RT, bool PACKED, int L>
 __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int block) {
-  constexpr int RG = NT / 4, F = 8;                           // rows side by side; rows in flight
-  __shared__ float part[NT / 64][32];
-  const int64_t width = a.width, nblk = mx_blocks(width), c = (int64_t)block * 32 + (threadIdx.x & 3) * 8;
+  constexpr int NT = norm_threads(L), GL = gain_lanes(L), C = 8 * GL;
+  constexpr int RG = NT / GL, F = 8;                          // rows side by side; rows in flight
+  __shared__ float part[NT / 64][C];
+  const int64_t width = a.width, nblk = mx_blocks(width), c = (int64_t)block * C + (threadIdx.x & (GL - 1)) * 8;
   const int m = (int)min<int64_t>(max<int64_t>(width - c, 0), 8);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const YT* const dy = static_cast<const YT*>(a.dy);
   const RT* const x = static_cast<const RT*>(a.x);
-  for (int64_t r0 = threadIdx.x >> 2; r0 < a.n; r0 += F * RG) {
+  for (int64_t r0 = threadIdx.x / GL; r0 < a.n; r0 += F * RG) {
     Raw8<YT> ry[F];
     Raw8<RT> rx[F];
     u32x2_t rq[F];
@@ -64,16 +70,16 @@ __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int block) {
     }
   }
 #pragma unroll
-  for (int o = 4; o < 64; o *= 2)
+  for (int o = GL; o < 64; o *= 2)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor(acc[j], o, 64);
-  if ((threadIdx.x & 63) < 4) {
+  if ((threadIdx.x & 63) < GL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[threadIdx.x >> 6][(threadIdx.x & 3) * 8 + j] = acc[j];
+    for (int j = 0; j < 8; ++j) part[threadIdx.x >> 6][(threadIdx.x & (GL - 1)) * 8 + j] = acc[j];
   }
   __syncthreads();
-  const int64_t at = (int64_t)block * 32 + threadIdx.x;
-  if (threadIdx.x < 32 && at < width) {
+  const int64_t at = (int64_t)block * C + threadIdx.x;
+  if (threadIdx.x < C && at < width) {
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < NT / 64; ++k) t += part[k][threadIdx.x];
@@ -89,7 +95,7 @@ __global__ __launch_bounds__(norm_threads(L)) void k_rms_norm_grad(const NormGra
   constexpr int NT = norm_threads(L), G = NT / L;
   if constexpr (COLS) {
     if ((int)blockIdx.x >= blocks) {
-      gain_columns<YT, RT, PACKED, NT>(a, (int)blockIdx.x - blocks);
+      gain_columns<YT, RT, PACKED, L>(a, (int)blockIdx.x - blocks);
       return;
     }
   }
@@ -217,7 +223,8 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
   return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto lanes, auto ch) {
     constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, NT = norm_threads(L);
     if (columns) {
-      const int64_t sums = (a.width + 31) / 32;
+      constexpr int C = 8 * gain_lanes(L);
+      const int64_t sums = (a.width + C - 1) / C;
       k_rms_norm_grad<YT, RT, PACKED, true, false, true, L, CH><<<dim3((uint32_t)(blocks + sums)), NT, 0, s>>>(a, blocks);
     } else {
       k_rms_norm_grad<YT, RT, PACKED, decltype(tail)::value, decltype(once)::value, false, L, CH>
