@@ -41,7 +41,7 @@ bool bad_outputs(const Span* outs, int no, const Span* ins, int ni, const Span* 
 struct WgradPlan {
   bool copy_dz, turn;
   int64_t npad, ldxt, lddz, dfull, ldp, whole, xt, dzt, part, bytes;
-  int splits, tile;
+  int splits, first, tile;
 };
 
 int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
@@ -55,37 +55,49 @@ int check_wgrad(const void* dz, int64_t n, int64_t rows, int64_t width) {
 }
 
 // Tile and parts of the tokens, by an estimate of the call's time in microseconds,
-// within some 15% of what these took (8192 x 2304 x 768: 256 tiles in 9 parts 59, 128
-// in 4 parts 53, 64 whole 55; 2048 x 768 x 768: 35, 19 and 14; 512 x 4096 x 4096: 37,
-// 36 and 51; 2048 x 14336 x 4096: 245, 284).  A stage of 64 tokens of a 256 tile
-// takes 1.55 on its own compute unit, with x brought to bf16 by a launch before it
-// (3 bytes a value); of a 128 tile 0.72, or 1.1 of the two that share a unit; of a 64
-// tile 0.28.  Each tile has an epilogue, the result is stored at 5 GB/ms (2.5
-// from the registers of a 256 tile), and parts cost a launch and are written and read.
+// within some 15% of what these took (8192 x 2304 x 768: 256 tiles in 9 parts 60, 128
+// in 4 parts 56, 64 whole 63; 2048 x 2304 x 768: 40, 28 and 20; 512 x 4096 x 4096: 37
+// and 32; 16384 x 2048 x 2048: 157 in 4 parts, 175; 8192 x 9000 x 2100: 319, 416).  A stage
+// of 64 tokens of a 256 tile takes 1.55 on its own compute unit, with x brought to bf16
+// by a launch before it (3 bytes a value); of a 128 tile 0.72, or 1.25 of the two that
+// share a unit; of a 64 tile 0.28.  Each tile has an epilogue, the result is stored at
+// 5 GB/ms (2.5 for 256 tiles), and parts cost a launch and are written and read.
+//
+// 256 tiles that fill the compute units once or more are whole, and those left over are cut
+// by themselves, against a round in which units are idle and the others run some 15%
+// faster (8192 x 14336 x 4096, 3 rounds and 128 tiles: whole 930, those in 2 parts 863; 8192 x 4352 x
+// 4096, 1 round and 16 tiles: whole 407, in 8 parts 274; 8192 x 5120 x 5120, 1 round and
+// 144 tiles: whole 420, in 3 parts 451).
 struct WgradChoice {
-  int tile, splits;
+  int tile, splits, first;
 };
 WgradChoice wgrad_choice(int64_t n, int64_t rows, int64_t width) {
   const int64_t stages = up(n, kXStage) / kXStage;
   const double values = (double)rows * (double)width;
-  WgradChoice best{kXTile, 1};
+  WgradChoice best{kXTile, 1, 0};
   double least = 0;
   for (const int tile : {256, 128, 64}) {
     const int64_t tiles = up(rows, tile) / tile * (up(width, tile) / tile);
     if (tile != kXTile && tiles > 64 * kXCus) continue;
+    const int64_t first = tile == kXTile ? tiles / kXCus * kXCus : 0, cut = tiles - first;
     for (int64_t k = 1; k <= 32 && k <= std::max<int64_t>(stages, 1); ++k) {
-      if (k > 1 && tiles * k > 4 * kXCus) break;
+      if (k > 1 && (cut == 0 || cut * k > 4 * kXCus)) break;
       const double each = (double)((stages + k - 1) / k);
       // tiles of the busiest unit; many tiles even out
-      const double c = tiles * k > 4 * kXCus ? (double)(tiles * k) / kXCus : (double)((tiles * k + kXCus - 1) / kXCus);
+      const double c = cut * k > 4 * kXCus ? (double)(cut * k) / kXCus : (double)((cut * k + kXCus - 1) / kXCus);
       double t;
-      if (tile == 256) t = 8.0 + 3.0 * (double)n * (double)width / 3.5e6 + c * (1.55 * each + 5.0) + 2.0 * values / 2.5e6;
-      else if (tile == 128) t = 3.5 + (c > 4 ? 0.55 * c : c == 1 ? 0.72 : c == 2 ? 1.1 : c == 3 ? 1.82 : 2.2) * each + 0.8 * (c + 1) + 2.0 * values / 5e6;
-      else t = 3.2 + c * (0.28 * each + 0.6) + 2.0 * values / 5e6;
-      if (k > 1) t += 3.0 + 8.0 * (double)k * values / 6e6;
+      if (tile == kXTile)
+        t = 8.0 + 3.0 * (double)n * (double)width / 3.5e6 + (double)(first / kXCus) * (1.55 * (double)stages + 5.0) +
+            c * ((first && k == 1 ? 1.32 : 1.55) * each + 5.0) + 2.0 * values / 2.5e6;
+      else if (tile == 128)
+        t = 3.5 + (c > 4 ? 0.64 * c : c == 1 ? 0.72 : c == 2 ? 1.25 : c == 3 ? 1.82 : 2.5) * each + 0.8 * (c + 1) +
+            2.0 * values / 5e6;
+      else
+        t = 3.2 + c * (0.28 * each + 0.6) + 2.0 * values / 5e6;
+      if (k > 1) t += 3.0 + 8.0 * (double)k * (tile == kXTile ? (double)cut * (kXTile * kXTile) : values) / 6e6;
       if (least == 0 || t < least) {
         least = t;
-        best = {tile, (int)k};
+        best = {tile, (int)k, (int)(k > 1 ? first : 0)};
       }
     }
   }
@@ -104,6 +116,7 @@ WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
   const WgradChoice c = wgrad_choice(n, rows, width);
   p.tile = c.tile;
   p.splits = c.splits;
+  p.first = c.first;
   // The smaller tiles' reads run over a row's end by less than a tile: the last
   // rows that this leaves the buffers from are in stages read value by value.
   auto behind = [&](int64_t row, int64_t over) { return (over + row - 1) / row; };
@@ -128,7 +141,8 @@ WgradPlan wgrad_plan(const void* dz, int64_t n, int64_t rows, int64_t width) {
   p.xt = take(large && n ? 2 * up(width, kXTile) * p.ldxt : 0);
   p.turn = large && wgrad_turns(width);
   p.dzt = take(!large || n == 0 ? 0 : p.turn ? 2 * up(rows, kXTile) * p.ldxt : 2 * (p.npad - p.dfull) * p.lddz);
-  p.part = take(p.splits > 1 ? 4 * p.splits * rows * p.ldp : 0);
+  const int64_t cut = up(width, kXTile) / kXTile * (up(rows, kXTile) / kXTile) - p.first;
+  p.part = take(p.splits == 1 ? 0 : large ? 4 * p.splits * cut * (kXTile * kXTile) : 4 * p.splits * rows * p.ldp);
   p.bytes = std::max<int64_t>(at, 256);
   return p;
 }
@@ -311,6 +325,7 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   a.dw_dt = internal_dtype(dw_dtype);
   a.accumulate = accumulate;
   a.splits = p.splits;
+  a.first = p.first;
   a.tile = p.tile;
   a.turn = p.turn ? 1 : 0;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -9,7 +9,9 @@
 // tokens too where x is so wide that the plain reads are worth a pass (api_act.hip);
 // sums in fp32.
 // The gain is a factor of the result's columns.  Weights of few tiles have their
-// tokens cut into parts, one product each, that a second launch adds in order.
+// tokens cut into parts, one product each, that a second launch adds in order; so
+// have the tiles of a large weight that are left over when the others fill the
+// compute units.
 #include <algorithm>
 
 #include "common.h"
@@ -141,9 +143,11 @@ __device__ __forceinline__ void stage_tile(float* tile, int di, int dj, const f3
 }
 
 // Stores ROWS rows of a tile from LDS by whole rows (from the registers a store
-// instruction would reach 32 bytes of each of 32 rows).
+// instruction would reach 32 bytes of each of 32 rows): to dw, or as sums of one part of the
+// tokens to `part`, rows of ldp.
 template <typename WT, int T, int ROWS, int THREADS>
-__device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t i0, int64_t o0, const float* tile) {
+__device__ __forceinline__ void put_rows(const WgradArgs& a, float* part, int64_t ldp, int64_t i0, int64_t o0,
+                                         const float* tile) {
   constexpr int C = T / 8, R = THREADS / C;                   // chunks of a row, rows at a time
   const int c = threadIdx.x % C * 8, r0 = threadIdx.x / C;
   const int64_t d = i0 + c;
@@ -157,18 +161,16 @@ __device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t 
     }
   };
   float e[8];
-  if (a.splits > 1) {
-    float* const out = a.part + (int64_t)split * a.rows * a.ldp;
-    if (d >= a.ldp) return;
+  const int m = (int)min<int64_t>(a.width - d, 8);
+  if (m <= 0) return;
+  if (part != nullptr) {
 #pragma unroll 2
     for (int r = r0; r < ROWS && o0 + r < a.rows; r += R) {
       row(r, e);
-      store8(out, (o0 + r) * a.ldp + d, e);
+      store8(part, r * ldp + c, e);
     }
     return;
   }
-  const int m = (int)min<int64_t>(a.width - d, 8);
-  if (m <= 0) return;
   float f[8];
   if (a.gain != nullptr) load_first(a.gain, d, m, f);
 #pragma unroll
@@ -192,7 +194,8 @@ __device__ __forceinline__ void put_rows(const WgradArgs& a, int split, int64_t 
   }
 }
 
-// One 256 x 256 tile over one part of the tokens.
+// One 256 x 256 tile; those from a.first on, which would not fill the compute units once
+// more, over one part of the tokens.
 template <typename WT, bool TURN>
 __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_wgrad(const WgradArgs a, int ni,
                                                                                              int no) {
@@ -201,26 +204,35 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
   constexpr int MI = 4, NI = 2, WM = Waves<MI, NI>::WM, WN = Waves<MI, NI>::WN;
   const int wave = threadIdx.x >> 6;
   const int wm = wave / Waves<MI, NI>::GN, wn = wave % Waves<MI, NI>::GN;
-  const int job = xcd_job(blockIdx.x, gridDim.x), per = ni * no, split = job / per;
+  const int all = (int)(a.npad / kXStage), first = a.first;
+  int tile_id, s0 = 0, s1 = all;
+  float* part = nullptr;
+  if ((int)blockIdx.x < first) {
+    tile_id = xcd_job(blockIdx.x, first);
+  } else {
+    const int job = xcd_job(blockIdx.x - first, gridDim.x - first), cut = ni * no - first, split = job / cut;
+    tile_id = first + job - split * cut;
+    s0 = (int)((uint32_t)(all * split) / (uint32_t)a.splits);
+    s1 = (int)((uint32_t)(all * (split + 1)) / (uint32_t)a.splits);
+    if (a.splits > 1) part = a.part + (int64_t)job * (kXTile * kXTile);
+  }
   int to, ti;
-  block_order(job - split * per, ni, no, ti, to);
+  block_order(tile_id, ni, no, ti, to);
   const int64_t i0 = (int64_t)ti * kXTile, o0 = (int64_t)to * kXTile;
-  const int all = (int)(a.npad / kXStage);
-  const int64_t s0 = (uint32_t)(all * split) / (uint32_t)a.splits, s1 = (uint32_t)(all * (split + 1)) / (uint32_t)a.splits;
-  const uint16_t* const xt = a.xt + i0 * a.ldxt + s0 * kXStage;
+  const uint16_t* const xt = a.xt + i0 * a.ldxt + (int64_t)s0 * kXStage;
   f32x16_t acc[MI][NI];
   if constexpr (TURN) {
-    const uint16_t* const dzt = a.dzt + o0 * a.ldxt + s0 * kXStage;
+    const uint16_t* const dzt = a.dzt + o0 * a.ldxt + (int64_t)s0 * kXStage;
     product<false, false, MI, NI>(
-        smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
+        smem, s1 - s0, [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
         [=](int s) { return dzt + (int64_t)s * kXStage; }, a.ldxt, 0, acc);
   } else {
     const uint16_t *const dz = a.dz + o0, *const dzc = a.dzt + o0;
     const int64_t full = a.dfull, ld = a.lddz;
     product<false, true, MI, NI>(
-        smem, (int)(s1 - s0), [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
+        smem, s1 - s0, [=](int s) { return xt + (int64_t)s * kXStage; }, a.ldxt, 0,
         [=](int s) {
-          const int64_t t = (s0 + s) * kXStage;
+          const int64_t t = (int64_t)(s0 + s) * kXStage;
           return t < full ? dz + t * ld : dzc + (t - full) * ld;
         },
         ld, ld - o0, acc);
@@ -233,7 +245,7 @@ __global__ __launch_bounds__(kXThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     __syncthreads();
     if (wm == h) stage_tile<WM>(tile, 0, wn * WN, acc);
     __syncthreads();
-    put_rows<WT, WM, kXTile, kXThreads>(a, split, i0 + h * WM, o0, tile);
+    put_rows<WT, WM, kXTile, kXThreads>(a, part == nullptr ? nullptr : part + h * WM, kXTile, i0 + h * WM, o0, tile);
   }
 }
 
@@ -455,19 +467,35 @@ __global__ __launch_bounds__(kDThreads) __attribute__((amdgpu_waves_per_eu(2))) 
     stage_tile<T>(tile, 32 * (wave >> 1), 32 * (wave & 1), mine);
   }
   __syncthreads();
-  put_rows<WT, T, T, kDThreads>(a, split, i0, o0, tile);
+  float* const part = a.splits > 1 ? a.part + ((int64_t)split * a.rows + o0) * a.ldp + i0 : nullptr;
+  put_rows<WT, T, T, kDThreads>(a, part, a.ldp, i0, o0, tile);
 }
 
 // dw from the parts: 4 columns a thread, 8 parts in flight, added in their order.
-template <typename WT>
-__global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a) {
-  const uint32_t per = (uint32_t)(a.ldp / 4), id = blockIdx.x * 256 + threadIdx.x;
-  const int64_t o = id / per, d = (int64_t)(id % per) * 4;
+// TILES: of the 256 tiles from a.first on, ni x no in all.
+template <typename WT, bool TILES>
+__global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a, int ni, int no) {
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x;
+  int64_t o, d, step;
+  const float* p;
+  if constexpr (TILES) {
+    const int t = (int)(id / (kXTile * kXTile / 4));
+    int to, ti;
+    block_order(a.first + t, ni, no, ti, to);
+    o = (int64_t)to * kXTile + id / (kXTile / 4) % kXTile;
+    d = (int64_t)ti * kXTile + id % (kXTile / 4) * 4;
+    step = (int64_t)(ni * no - a.first) * (kXTile * kXTile);
+    p = a.part + (int64_t)id * 4;
+  } else {
+    const uint32_t per = (uint32_t)(a.ldp / 4);
+    o = id / per;
+    d = (int64_t)(id % per) * 4;
+    step = a.rows * a.ldp;
+    p = a.part + o * a.ldp + d;
+  }
   if (o >= a.rows) return;
   const int m = (int)min<int64_t>(a.width - d, 4);
   if (m <= 0) return;
-  const int64_t step = a.rows * a.ldp;
-  const float* p = a.part + o * a.ldp + d;
   f32x4_t e = {0.f, 0.f, 0.f, 0.f};
   for (int k = 0; k < a.splits; k += 8, p += 8 * step) {
     f32x4_t r[8];
@@ -518,14 +546,18 @@ namespace {
 template <typename WT>
 hipError_t wgrad(const WgradArgs& a, hipStream_t s) {
   const int ni = (int)((a.width + a.tile - 1) / a.tile), no = (int)((a.rows + a.tile - 1) / a.tile);
-  const dim3 g((uint32_t)((int64_t)ni * no * a.splits));
+  const int64_t cut = (int64_t)ni * no - a.first;  // tiles in parts
+  const dim3 g((uint32_t)(a.first + cut * a.splits));
   if (a.tile == kXTile && a.turn) k_wgrad<WT, true><<<g, kXThreads, 0, s>>>(a, ni, no);
   else if (a.tile == kXTile) k_wgrad<WT, false><<<g, kXThreads, 0, s>>>(a, ni, no);
   else if (a.tile == 128) k_wgrad_direct<WT, 128><<<g, kDThreads, 0, s>>>(a, ni, no);
   else k_wgrad_direct<WT, 64><<<g, kDThreads, 0, s>>>(a, ni, no);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  k_wgrad_join<WT><<<dim3((uint32_t)((a.rows * (a.ldp / 4) + 255) / 256)), 256, 0, s>>>(a);
+  if (a.tile == kXTile)
+    k_wgrad_join<WT, true><<<dim3((uint32_t)(cut * (kXTile * kXTile / 4 / 256))), 256, 0, s>>>(a, ni, no);
+  else
+    k_wgrad_join<WT, false><<<dim3((uint32_t)((a.rows * (a.ldp / 4) + 255) / 256)), 256, 0, s>>>(a, ni, no);
   return hipGetLastError();
 }
 }  // namespace

@@ -19,9 +19,10 @@ struct WgradArgs {
   uint16_t* xt;                      // width up to a tile rows of ldxt: q's values in bf16 along the tokens
   uint16_t* dzt;                     // turn: dz along the tokens, rows up to a tile of ldxt; else dz's rows [dfull, n),
                                      // padded with zeros to a whole stage, of lddz
-  float* part;                       // [splits][rows][ldp], with splits > 1
+  float* part;                       // with splits > 1: [splits][rows][ldp], or [splits][256 tiles from first on][256][256]
   int64_t n, npad, rows, width, ldxt, lddz, dfull, ldp;
   int64_t whole;                     // stages that the 64 and 128 tiles read whole, over the rows' ends
+  int32_t first;                     // 256 tiles before this one (in the order of the jobs) are not cut into parts
   float scale;
   int32_t dw_dt, accumulate, splits, turn, tile;  // tile: 256 (from xt and dz or dzt), or 128 or 64 from q and dz
 };

@@ -104,6 +104,21 @@ def test_wide(n, rows, width, off):
     check(mm.weight_grad(dz, p, out=acc, accumulate=True, scale=-2.0), dz, p, None, -2.0, base)
 
 
+@pytest.mark.parametrize("n,rows,width", [(4099, 4107, 4090), (4160, 4104, 4096), (6150, 2100, 8440)])
+def test_tiles_left_over(n, rows, width):
+    """Sizes of 272 or 297 tiles: those behind the first 256 are cut into parts."""
+    print(f"[case] weight gradient, tiles left over {n} {rows} {width}", flush=True)
+    dz, p, gain = inputs(n, rows, width)
+    left = (rows + 255) // 256 * ((width + 255) // 256) - 256
+    parts = mm.load().muonh_weight_grad_workspace(dz.data_ptr(), n, rows, width) - 2 * width * n
+    parts -= 2 * n * rows if rows % 8 or width >= 8192 else 2 * (n % 64) * rows
+    assert 0 < left <= 41 and parts >= 2 * left * 4 * 65536
+    check(mm.weight_grad(dz, p, gain=gain, out_dtype=F32), dz, p, gain)
+    base = torch.randn(rows, width, device=DEV).bfloat16()
+    acc = base.clone()
+    check(mm.weight_grad(dz, p, out=acc, accumulate=True, scale=-2.0), dz, p, None, -2.0, base)
+
+
 def test_of_the_norm():
     """From what the norm kept: the gradient behind its output."""
     print("[case] weight gradient behind the norm", flush=True)
