@@ -163,7 +163,10 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
   const int64_t each = sizeof(XT) + (RES ? 2 * sizeof(RT) : 0) + (a.y ? (a.y_dt == DT_BF16 ? 2 : 4) : 0) + (a.q ? 1 : 0);
   return with_shape(a.width, a.n * a.width * each > kActOnceBytes, [&](auto tail, auto once, auto lanes, auto ch) {
     constexpr int L = decltype(lanes)::value, CH = decltype(ch)::value, NT = norm_threads(L), G = NT / L;
-    const int64_t blocks = std::min<int64_t>((a.n + G - 1) / G, 2048);
+    // a row of 1024 threads is worth its workgroup's start less often (at most 1024, 2048 and 8192
+    // workgroups: 4096 x 16384 105, 108 and 114 us, 16384 x 4096 100, 99 and 97, 8000 x 1999 fp32
+    // 53, 60 and 54, 8192 x 768 18, 16.0 and 15.8)
+    const int64_t blocks = std::min<int64_t>((a.n + G - 1) / G, L == 1024 ? 1024 : 8192);
     k_rms_norm<XT, RT, RES, decltype(tail)::value, decltype(once)::value, L, CH><<<dim3((uint32_t)blocks), NT, 0, s>>>(a);
     return hipGetLastError();
   });
