@@ -4,10 +4,13 @@
 // threads of a block of 32 find its largest magnitude by lane exchanges, and
 // the values leave as 8 bytes with one scale byte a block.  A row belongs to a power of two of
 // threads, so that short rows share a workgroup and nothing is divided; a
-// thread has kRows rows in flight.  Matrices beyond the last-level cache are
-// read and written past the caches (ONCE).  16 values a thread, two stores of every
-// other 16 bytes of a line, took longer: 8192 x 14336 to bf16 77 us (ONCE: 127) against
-// 72, 1021 x 331 fp32 to 8 bits 7.1 against 4.4.
+// thread has kRows rows in flight.  A workgroup's rows are neighbours and those
+// side by side over a row follow each other, so that what is in flight at a time is one
+// stretch of memory (rows of a workgroup as far apart as the grid is long: 8192 x 14336
+// to bf16 71 us and not 61, 16384 x 4096 fp32 to 8 bits 76 and not 67).  Matrices
+// beyond the last-level cache are read and written past the caches (ONCE).  16
+// values a thread, two stores of every other 16 bytes of a line, took longer: 8192 x
+// 14336 to bf16 by 7% (ONCE: 76%), 1021 x 331 fp32 to 8 bits 7.1 us against 4.4.
 #include <algorithm>
 #include <type_traits>
 
@@ -29,24 +32,25 @@ int row_log(int64_t width) {
 }
 
 template <typename T, bool ONCE>
-__global__ __launch_bounds__(256) void k_mx_pack(const MxArgs a, int lg) {
+__global__ __launch_bounds__(256) void k_mx_pack(const MxArgs a, int lg, uint32_t side) {
   const int64_t width = a.width, nblk = mx_blocks(width);
   const T* const in = static_cast<const T*>(a.in);
-  const int64_t c = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+  const uint32_t down = blockIdx.x / side;
+  const int64_t c = ((int64_t)(blockIdx.x - down * side) << lg) + (threadIdx.x & ((1 << lg) - 1));
   const int m = (int)min<int64_t>(max<int64_t>(width - 8 * c, 0), 8);
-  const int64_t per = 256 >> lg, step = per * gridDim.x;
-  for (int64_t r0 = blockIdx.x * per + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * step) {
+  const int64_t per = 256 >> lg, all = per * (gridDim.x / side);
+  for (int64_t r0 = (int64_t)down * per * kRows + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * all) {
     Raw8<T> raw[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u)
-      if (m == 8 && r0 + u * step < a.n) {
-        const int64_t at = (r0 + u * step) * width + 8 * c;
+      if (m == 8 && r0 + u * per < a.n) {
+        const int64_t at = (r0 + u * per) * width + 8 * c;
         if constexpr (ONCE) raw[u].load_once(in, at);
         else raw[u].load_any(in, at);
       }
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + u * step;
+      const int64_t r = r0 + u * per;
       if (r >= a.n) break;  // the same for the 4 lanes of a block
       float v[8];
       if (m == 8) raw[u].unpack(v);
@@ -61,19 +65,20 @@ __global__ __launch_bounds__(256) void k_mx_pack(const MxArgs a, int lg) {
 }
 
 template <typename T, bool ONCE>
-__global__ __launch_bounds__(256) void k_mx_unpack(const MxArgs a, int lg) {
+__global__ __launch_bounds__(256) void k_mx_unpack(const MxArgs a, int lg, uint32_t side) {
   const int64_t width = a.width, nblk = mx_blocks(width);
   T* const out = static_cast<T*>(a.out);
-  const int64_t c = ((int64_t)blockIdx.y << lg) + (threadIdx.x & ((1 << lg) - 1));
+  const uint32_t down = blockIdx.x / side;
+  const int64_t c = ((int64_t)(blockIdx.x - down * side) << lg) + (threadIdx.x & ((1 << lg) - 1));
   const int m = (int)min<int64_t>(max<int64_t>(width - 8 * c, 0), 8);
   if (m == 0) return;
-  const int64_t per = 256 >> lg, step = per * gridDim.x;
-  for (int64_t r0 = blockIdx.x * per + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * step) {
+  const int64_t per = 256 >> lg, all = per * (gridDim.x / side);
+  for (int64_t r0 = (int64_t)down * per * kRows + (threadIdx.x >> lg); r0 < a.n; r0 += kRows * all) {
     u32x2_t q[kRows];
     uint32_t sc[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + u * step;
+      const int64_t r = r0 + u * per;
       if (r < a.n) {
         sc[u] = gmem(a.scales)[r * nblk + c / 4];
         q[u] = m == 8 ? load_q8(a.q + r * width + 8 * c) : load_q8(a.q + r * width + 8 * c, m);
@@ -81,7 +86,7 @@ __global__ __launch_bounds__(256) void k_mx_unpack(const MxArgs a, int lg) {
     }
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + u * step;
+      const int64_t r = r0 + u * per;
       if (r >= a.n) break;
       float v[8];
       from_e4m3(q[u], mx_factor(sc[u]), v);
@@ -92,11 +97,13 @@ __global__ __launch_bounds__(256) void k_mx_unpack(const MxArgs a, int lg) {
   }
 }
 
-// Workgroups side by side over a row, and over the rows.
+// Workgroups side by side over a row.
+uint32_t across(int64_t width, int lg) { return (uint32_t)((width + ((int64_t)8 << lg) - 1) / ((int64_t)8 << lg)); }
+// Those over all rows.
 dim3 grid(const MxArgs& a, int lg) {
-  const int64_t across = (a.width + ((int64_t)8 << lg) - 1) / ((int64_t)8 << lg), per = 256 >> lg;
-  const int64_t down = std::min<int64_t>((a.n + per * kRows - 1) / (per * kRows), std::max<int64_t>(1, 65536 / across));
-  return dim3((uint32_t)down, (uint32_t)across);
+  const int64_t side = across(a.width, lg), per = 256 >> lg;
+  const int64_t down = std::min<int64_t>((a.n + per * kRows - 1) / (per * kRows), std::max<int64_t>(1, 65536 / side));
+  return dim3((uint32_t)(down * side));
 }
 
 // f with std::true_type where `bytes` are moved that no cache holds.
@@ -111,8 +118,8 @@ void past_caches(int64_t bytes, F&& f) {
 hipError_t launch_mx_pack(int dt, const MxArgs& a, hipStream_t s) {
   const int lg = row_log(a.width);
   past_caches(a.n * a.width * (dt == DT_BF16 ? 3 : 5), [&](auto once) {
-    if (dt == DT_BF16) k_mx_pack<bf16_t, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg);
-    else k_mx_pack<float, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg);
+    if (dt == DT_BF16) k_mx_pack<bf16_t, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg, across(a.width, lg));
+    else k_mx_pack<float, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg, across(a.width, lg));
   });
   return hipGetLastError();
 }
@@ -120,8 +127,8 @@ hipError_t launch_mx_pack(int dt, const MxArgs& a, hipStream_t s) {
 hipError_t launch_mx_unpack(int dt, const MxArgs& a, hipStream_t s) {
   const int lg = row_log(a.width);
   past_caches(a.n * a.width * (dt == DT_BF16 ? 3 : 5), [&](auto once) {
-    if (dt == DT_BF16) k_mx_unpack<bf16_t, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg);
-    else k_mx_unpack<float, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg);
+    if (dt == DT_BF16) k_mx_unpack<bf16_t, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg, across(a.width, lg));
+    else k_mx_unpack<float, decltype(once)::value><<<grid(a, lg), 256, 0, s>>>(a, lg, across(a.width, lg));
   });
   return hipGetLastError();
 }
