@@ -137,9 +137,11 @@ def test_limits_and_workspace():
     assert size(0, -1, 8, 8) == size(0, 8, 0, 8) == size(0, 8, 8, 0) == size(0, (1 << 22) + 1, 8, 8) == size(1, 8, 8, 8) == 0
     assert weight(ws_bytes=size(A, 4, 24, 40) - 1) == mm.MUONH_ENOMEM
     assert weight(n=0, acc=1, dz=None, q=None, scales=None) == mm.MUONH_OK
-    # x in bf16, once; dz again where its rows are off the grid; never a share that grows with more than the sizes
+    # x in bf16, once; dz again where its rows are off the grid; never a share that grows with more than the sizes.
+    # 56 x 16 tiles of 256 are 3 rounds of 256 and 128 tiles, these in two parts of 4 bytes a value
     n, rows, width = 8192, 14336, 4096
-    assert size(0, n, rows, width) <= 2 * width * (n + 192) + 4096
+    assert size(0, n, rows, width) <= 2 * width * (n + 192) + 2 * 128 * 4 * 256 * 256 + 4096
+    assert size(0, n, 16 * 256, width) <= 2 * width * (n + 192) + 4096
     assert size(2, n, rows, width) >= 2 * n * (rows + width)
     assert size(0, n, rows + 1, width) >= 2 * n * (rows + width)
 
