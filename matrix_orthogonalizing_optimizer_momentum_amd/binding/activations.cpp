@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <optional>
 #include <string>
 
 #include "muonh.h"
@@ -98,7 +99,8 @@ float* gain_of(PyObject* o, int64_t width, int dev, const char* what = "gain") {
   return static_cast<float*>(g.data_ptr());
 }
 
-// A pair (values, scales); holds the references that the pair may give up.
+// A pair (values, scales).  It may be any sequence or iterator, which makes its tensors on
+// access and keeps none of them: a Pair holds them, and lives until its call's work is queued.
 struct Pair {
   PyObject* seq;
   const at::Tensor *q, *s;
@@ -296,12 +298,13 @@ PyObject* muonh_py_rms_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t na) {
                                          : dres.defined() ? dres.scalar_type()
                                                           : dy.scalar_type());
     const void *x = nullptr, *q = nullptr, *s = nullptr;
+    std::optional<Pair> pair;
     if (direct) {
       const at::Tensor& v = THPVariable_Unpack(a[2]);
       like(v, dy, "x", dev, t);
       x = v.data_ptr();
     } else {
-      const Pair p(a[2], "x", dev);
+      const Pair& p = pair.emplace(a[2], "x", dev);
       if (p.q->sizes() != dy.sizes()) value_error("x must have the shape of dy");
       q = p.q->data_ptr();
       s = p.s->data_ptr();

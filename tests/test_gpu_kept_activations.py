@@ -1,0 +1,53 @@
+"""What the operators between the embedding and the output layer are handed in other ways
+than a program's own tuple of tensors."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import matrix_orthogonalizing_optimizer_momentum_amd as mm  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+class Fetched:
+    """A pair that makes its tensors on access and keeps none, as one brought back from
+    elsewhere would."""
+
+    def __init__(self, packed):
+        self.kept = packed
+
+    def __len__(self):
+        return 2
+
+    def __getitem__(self, k):
+        if k > 1:
+            raise IndexError(k)
+        return self.kept[k].clone()
+
+
+# rows by columns in one launch; partial sums of 2.4 MB and more beside 8-bit rows of as much
+@pytest.mark.parametrize("n,width", [(300, 1100), (3100, 768), (8192, 768), (6000, 2048)])
+def test_pairs_that_keep_nothing(n, width):
+    """Tensors of a pair that nobody else holds last until the call's work is queued: its
+    outputs and scratch memory are not allocated over them."""
+    print(f"[case] pairs that keep nothing {n} {width}", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(n + width)
+    x = torch.randn(n, width, generator=g, device=DEV)
+    dy = torch.randn(n, width, generator=g, device=DEV).bfloat16()
+    dz = torch.randn(n, 200, generator=g, device=DEV).bfloat16()
+    gain = torch.rand(width, generator=g, device=DEV) + 0.5
+    r = mm.rms_norm(x, gain, pack="normalized", output=False)
+    want = mm.rms_norm_grad(dy, r.packed, r.rstd, gain, out_dtype=F32)
+    dw, back = mm.weight_grad(dz, r.packed), mm.mx_unpack(r.packed)
+    for _ in range(3):
+        for pair in (lambda: Fetched(r.packed), lambda: (t.clone() for t in r.packed), lambda: [t.clone() for t in r.packed]):
+            dx, dgain = mm.rms_norm_grad(dy, pair(), r.rstd, gain, out_dtype=F32)
+            assert torch.equal(dx, want[0]) and torch.equal(dgain, want[1])
+            assert torch.equal(mm.weight_grad(dz, pair()), dw)
+        assert torch.equal(mm.mx_unpack(Fetched(r.packed)), back)
+        del dx, dgain
+    with pytest.raises(ValueError, match="pair"):
+        mm.rms_norm_grad(dy, iter(r.packed[:1]), r.rstd, gain)
