@@ -506,7 +506,8 @@ int muonh_rms_norm(const void* x, int x_dtype, const void* residual, int h_dtype
  *   dres      device, n x width of dx_dtype, or NULL
  *   dx        device, n x width of dx_dtype; may be dres
  *   dgain     device, width floats, or NULL; accumulate = 1 adds to it
- *   workspace needed with dgain
+ *   workspace needed with dgain; must overlap no other buffer
+ * Other overlaps of an output are refused as by muonh_rms_norm.
  * Sums are fp32.  n = 0 clears dgain (or leaves it).
  */
 size_t muonh_rms_norm_grad_workspace(int64_t n, int64_t width);
@@ -534,6 +535,7 @@ int muonh_mx_unpack(const void* q, const void* scales, int64_t n, int64_t width,
  *   gain      device, width floats, or NULL (1);  scale  finite
  *   dw        device, rows x width of dw_dtype (MUONH_F32 / MUONH_BF16);
  *             accumulate = 1 adds to it; must not overlap the inputs
+ *   workspace must overlap no other buffer (MUONH_EINVAL, as for dw)
  *   n         0 .. 2^22;  rows, width  1 .. 2^20, together up to 2^37 values of dw
  *             and 2^35 of dz or x (MUONH_ENOTIMPL above); n = 0 clears dw (or leaves it)
  * Sums are fp32, rounded once.  Large products keep x in bf16 in the workspace, parts

@@ -25,8 +25,8 @@ int check_rows(int64_t n, int64_t width, int64_t max_width) {
 // A buffer of `bytes` aligned to `a`: given, unless it has none.
 bool bad_buffer(const void* p, int64_t bytes, int64_t a) { return bytes > 0 && (!p || misaligned(p, a)); }
 
-// Outputs apart from the inputs and from each other.  same[k]: the one input that
-// output k may be, value for value.
+// Outputs, scratch memory among them, apart from the inputs and from each other.
+// same[k]: the one input that output k may be, value for value.
 bool bad_outputs(const Span* outs, int no, const Span* ins, int ni, const Span* const* same) {
   for (int k = 0; k < no; ++k) {
     for (int i = 0; i < ni; ++i)
@@ -212,17 +212,18 @@ int muonh_rms_norm_grad(const void* dy, int dy_dtype, const void* x, const void*
   const int64_t sx = dtype_size(dx_dtype);
   if (bad_buffer(dy, n, dtype_size(dy_dtype)) || bad_buffer(rstd, n, 4) || bad_buffer(dx, n, sx)) return MUONH_EINVAL;
   if (misaligned(x, sx) || misaligned(dres, sx) || misaligned(gain, 4) || misaligned(dgain, 4)) return MUONH_EINVAL;
+  const size_t scratch = dgain ? muonh_rms_norm_grad_workspace(n, width) : 0;
   if (dgain) {
     if (!workspace || misaligned(workspace, 256)) return MUONH_EINVAL;
-    if (workspace_bytes < muonh_rms_norm_grad_workspace(n, width)) return MUONH_ENOMEM;
+    if (workspace_bytes < scratch) return MUONH_ENOMEM;
   }
   const int64_t all = n * width;
   const Span ins[] = {span_of(dy, all * dtype_size(dy_dtype)), span_of(x, all * sx), span_of(q, all),
                       span_of(scales, n * mx_blocks(width)), span_of(rstd, 4 * n), span_of(gain, 4 * width),
                       span_of(dres, all * sx)};
-  const Span outs[] = {span_of(dx, all * sx), span_of(dgain, 4 * width)};
-  const Span* const same[] = {&ins[6], nullptr};
-  if (bad_outputs(outs, 2, ins, 7, same)) return MUONH_EINVAL;
+  const Span outs[] = {span_of(dx, all * sx), span_of(dgain, 4 * width), span_of(workspace, (int64_t)scratch)};
+  const Span* const same[] = {&ins[6], nullptr, nullptr};
+  if (bad_outputs(outs, 3, ins, 7, same)) return MUONH_EINVAL;
   if (n == 0 && (!dgain || accumulate)) return MUONH_OK;
   NormGradArgs a{};
   a.dy = dy;
@@ -298,9 +299,9 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   if (workspace_bytes < (size_t)p.bytes) return MUONH_ENOMEM;
   const Span ins[] = {span_of(dz, 2 * n * rows), span_of(q, n * width), span_of(scales, n * mx_blocks(width)),
                       span_of(gain, 4 * width)};
-  const Span outs[] = {span_of(dw, rows * width * dtype_size(dw_dtype))};
-  const Span* const same[] = {nullptr};
-  if (bad_outputs(outs, 1, ins, 4, same)) return MUONH_EINVAL;
+  const Span outs[] = {span_of(dw, rows * width * dtype_size(dw_dtype)), span_of(workspace, p.bytes)};
+  const Span* const same[] = {nullptr, nullptr};
+  if (bad_outputs(outs, 2, ins, 4, same)) return MUONH_EINVAL;
   if (n == 0 && accumulate) return MUONH_OK;
   char* const ws = static_cast<char*>(workspace);
   WgradArgs a{};
