@@ -27,13 +27,25 @@ __device__ __forceinline__ double rsqrt64(double a) {
 // What becomes 8 bits is rounded to 4 significant ones.  Its fp32 value, a few roundings
 // off, decides as the exact one does unless it is within them of where two e4m3
 // values meet, whose last 19 bits are zeros: near_border tells (8 values: 1 wave in a
-// hundred), and such values are formed anew in fp64 and moved off the border to the
-// side where they lie.
+// hundred, and each that holds a 0, lanes behind the row's end among them), and such values
+// are formed anew in fp64 and moved off the border to the side where they lie.
 __device__ __forceinline__ bool near_border(const float (&v)[8]) {
   uint32_t low = ~0u;
 #pragma unroll
   for (int j = 0; j < 8; ++j) low = min(low, (__float_as_uint(v[j]) + 4) & 0x7ffffu);
   return low < 9;
+}
+// Those roundings are relative ones of normal numbers alone.  Below them are rstd where the row's
+// values are some 2^126 and more, and the product of rstd with a value other than 0 below 2^-126 / rstd,
+// which a gain may bring back: the bits of the values up to which a row is formed anew.
+__device__ __forceinline__ uint32_t anew_below(float rstd, bool gained) {
+  return rstd < 0x1p-126f ? 0x7f800000u : gained ? __float_as_uint(0x1p-125f * __builtin_amdgcn_rcpf(rstd)) : 0u;
+}
+__device__ __forceinline__ bool any_below(const float (&v)[8], uint32_t bits) {
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) low = min(low, (__float_as_uint(v[j]) & 0x7fffffffu) - 1);
+  return low < bits;
 }
 __device__ __forceinline__ float settle(double t) {
   const float f = (float)t;
@@ -136,7 +148,7 @@ __global__ __launch_bounds__(norm_threads(L)) void k_rms_norm(const NormArgs a) 
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = v[k][j] * rstd;
         }
-        if (near_border(y)) {
+        if (near_border(y) || any_below(v[k], anew_below(rstd, a.packs_output != 0))) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             // copies that the compiler does not see through: it would keep fp64 values of the
