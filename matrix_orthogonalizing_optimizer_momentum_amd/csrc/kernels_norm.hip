@@ -27,8 +27,8 @@ __device__ __forceinline__ double rsqrt64(double a) {
 // What becomes 8 bits is rounded to 4 significant ones.  Its fp32 value, a few roundings
 // off, decides as the exact one does unless it is within them of where two e4m3
 // values meet, whose last 19 bits are zeros: near_border tells (8 values: 1 wave in a
-// hundred, and each that holds a 0, lanes behind the row's end among them), and such values
-// are formed anew in fp64 and moved off the border to the side where they lie.
+// hundred, and each that has a 0 in its row), and such values are formed anew in fp64 and moved
+// off the border to the side where they lie.
 __device__ __forceinline__ bool near_border(const float (&v)[8]) {
   uint32_t low = ~0u;
 #pragma unroll
@@ -148,7 +148,8 @@ __global__ __launch_bounds__(norm_threads(L)) void k_rms_norm(const NormArgs a) 
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = v[k][j] * rstd;
         }
-        if (near_border(y) || any_below(v[k], anew_below(rstd, a.packs_output != 0))) {
+        // lanes behind the row's end hold zeros
+        if (m > 0 && (near_border(y) || any_below(v[k], anew_below(rstd, a.packs_output != 0)))) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             // copies that the compiler does not see through: it would keep fp64 values of the
