@@ -308,7 +308,7 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   a.dz = static_cast<const uint16_t*>(dz);
   a.q = static_cast<const uint8_t*>(q);
   a.scales = static_cast<const uint8_t*>(scales);
-  a.gain = gain;
+  a.gain = n > 0 ? gain : nullptr;  // of no tokens the sums stay 0, whatever the factors are
   a.dw = dw;
   a.xt = reinterpret_cast<uint16_t*>(ws + p.xt);
   a.dzt = reinterpret_cast<uint16_t*>(ws + p.dzt);
@@ -322,7 +322,7 @@ int muonh_weight_grad(const void* dz, const void* q, const void* scales, const f
   a.dfull = p.dfull;
   a.ldp = p.ldp;
   a.whole = p.whole;
-  a.scale = scale;
+  a.scale = n > 0 ? scale : 1.f;
   a.dw_dt = internal_dtype(dw_dtype);
   a.accumulate = accumulate;
   a.splits = p.splits;

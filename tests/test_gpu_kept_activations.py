@@ -51,3 +51,16 @@ def test_pairs_that_keep_nothing(n, width):
         del dx, dgain
     with pytest.raises(ValueError, match="pair"):
         mm.rms_norm_grad(dy, iter(r.packed[:1]), r.rstd, gain)
+
+
+def test_no_tokens_clear_the_gradient():
+    """Without a token there is nothing that a gain could scale, whatever it holds."""
+    print("[case] weight gradient of no tokens", flush=True)
+    gain = torch.ones(64, device=DEV)
+    gain[3], gain[7], gain[40] = float("inf"), float("nan"), -float("inf")
+    none = mm.mx_pack(torch.zeros(0, 64, device=DEV))
+    for rows in (16, 2000):
+        out = torch.full((rows, 64), 5.0, device=DEV)
+        assert mm.weight_grad(torch.zeros(0, rows, device=DEV, dtype=BF16), none, gain=gain, scale=-2.0, out=out) is out
+        assert torch.equal(out.view(torch.int32), torch.zeros(rows, 64, device=DEV, dtype=torch.int32))
+        assert bool((mm.weight_grad(torch.zeros(0, rows, device=DEV, dtype=BF16), none, gain=gain) == 0).all())
