@@ -47,6 +47,7 @@ from __future__ import annotations
 import ctypes
 import os
 from ctypes import POINTER, c_char, c_double, c_float, c_int, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
+from importlib import import_module
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuonh.so")
 
@@ -508,13 +509,16 @@ def profile_read():
     return out
 
 
+_GRADIENTS = frozenset(("clip_grads", "cross_entropy", "embedding", "embedding_grad", "grad_norm"))
+_ACTIVATIONS = frozenset(("Normed", "Packed", "mx_pack", "mx_unpack", "rms_norm", "rms_norm_grad", "weight_grad"))
+
+
 def __getattr__(name):
     # gradients.py and activations.py need torch at import, which nothing above does
-    if name in ("clip_grads", "cross_entropy", "embedding", "embedding_grad", "grad_norm"):
-        from . import gradients as module
-    elif name in ("Normed", "Packed", "mx_pack", "mx_unpack", "rms_norm", "rms_norm_grad", "weight_grad"):
-        from . import activations as module
-    else:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    globals()[name] = value = getattr(module, name)  # found without this function from now on (0.5 us a call)
-    return value
+    if name in _GRADIENTS:
+        # not kept: what takes a function's place in gradients.py is called from here too
+        return getattr(globals().get("gradients") or import_module(".gradients", __name__), name)
+    if name in _ACTIVATIONS:
+        globals()[name] = value = getattr(import_module(".activations", __name__), name)  # kept: 0.4 us a call less
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
