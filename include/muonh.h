@@ -469,7 +469,7 @@ int muonh_cross_entropy(const void* x, const void* w, const void* targets, int i
  *
  * muonh_rms_norm -- root-mean-square norm of the rows of x, or of the residual
  * stream that x is added to:
- *   h  = round(x + residual)   (to h's type; h = x without a residual)
+ *   h  = round(x + residual)   (their fp32 sum, to h's type; h = x without a residual)
  *   rstd = (mean_j h_j^2 + eps)^-1/2,  xn = rstd h,  y = gain xn
  *   x         device, n x width, MUONH_F32 or MUONH_BF16
  *   residual  device, n x width of h_dtype, with h, or both NULL

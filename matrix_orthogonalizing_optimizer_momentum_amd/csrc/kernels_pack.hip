@@ -10,7 +10,9 @@
 // to bf16 71 us and not 61, 16384 x 4096 fp32 to 8 bits 76 and not 67).  Matrices
 // beyond the last-level cache are read and written past the caches (ONCE).  16
 // values a thread, two stores of every other 16 bytes of a line, took longer: 8192 x
-// 14336 to bf16 by 7% (ONCE: 76%), 1021 x 331 fp32 to 8 bits 7.1 us against 4.4.
+// 14336 to bf16 by 7% (ONCE: 76%), 1021 x 331 fp32 to 8 bits 7.1 us against 4.4.  An fp32 result
+// is 32 bytes a thread and stored so all the same: 16384 x 4096 76 us, the bytes alone 49 at the
+// rate of a fill (from fp32 65).
 #include <algorithm>
 #include <type_traits>
 

@@ -75,6 +75,8 @@ __device__ __forceinline__ T row_sum(T v, T (*red)[row_waves(L)], int turn) {
   return s;
 }
 
+// fp32 chunks are two accesses of every other 16 bytes of a line, past the caches as well (norm of
+// 16384 x 4096 bf16 into an fp32 stream, with 8 bits: 157 us, the bytes alone 128).
 template <bool ONCE, typename T>
 __device__ __forceinline__ void load_chunk(Raw8<T>& r, const T* p, int64_t i) {
   if constexpr (ONCE) r.load_once(p, i);

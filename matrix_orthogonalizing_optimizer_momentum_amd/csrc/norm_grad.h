@@ -90,6 +90,12 @@ __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int block) {
 // RT: type of dx, dres and x (x: the norm's input; PACKED: xn in 8 bits instead).
 // COLS: workgroups behind the first `blocks` sum the gain's gradient by columns
 // (an instance of its own: the others need fewer registers).
+// A workgroup has one row in flight: the next one's loads wait for its sum and stores
+// (8192 x 768, 768 workgroups of 2 waves: 4.7 TB/s; 16384 x 4096, 512 of 8: 6.9).  Rows of 1024 threads have
+// 128 registers a lane, which two chunks of 8 columns (widths above 8192: gain, sums and three
+// operands of 16 columns) exceed by 10 to 87 (4096 x 16384 bf16 119 us, the bytes alone 69), and the
+// 8 rows in flight of gain_columns by 24 to 178 but for bf16 dy and x in 8 bits (256 x 5120 from
+// bf16 x 13 us, from fp32 x 23).
 template <typename YT, typename RT, bool PACKED, bool TAIL, bool ONCE, bool COLS, int L, int CH>
 __global__ __launch_bounds__(norm_threads(L)) void k_rms_norm_grad(const NormGradArgs a, int blocks) {
   constexpr int NT = norm_threads(L), G = NT / L;
