@@ -49,6 +49,12 @@ def _check(rc, where):
         raise MuonhError(rc, where)
 
 
+def _held(ts):
+    """A list or tuple of the tensors: any other sequence may make them on access, and they
+    have to last until the work that reads them is queued."""
+    return ts if isinstance(ts, (list, tuple)) else list(ts)
+
+
 def _table(ts, what):
     """(pointers, sizes, dtype codes, device) of a list of gradients, checked."""
     if _tensors is None:
@@ -66,6 +72,7 @@ def grad_norm(grads, max_norm=None, stream=None):
     to ``muonh_step`` / ``adamh_step`` as ``grad_scale`` to step on the clipped
     gradients without another pass over them.
     """
+    grads = _held(grads)
     n = len(grads)
     if n == 0:
         raise ValueError("no gradients")
@@ -91,12 +98,14 @@ def clip_grads(grads, max_norm, outputs=None, stream=None):
     ``outputs[i] = coef * grads[i]`` with ``grad_norm``'s coefficient;
     ``outputs=None`` scales ``grads`` in place.  Returns ``(total, coef)``.
     """
+    grads = _held(grads)
     n = len(grads)
     if n == 0:
         raise ValueError("no gradients")
     ptrs, sizes, codes, dev = _table(grads, "grads")
     outs = ptrs
     if outputs is not None:
+        outputs = _held(outputs)
         if len(outputs) != n:
             raise ValueError("outputs must have one tensor per gradient")
         outs, osizes, ocodes, odev = _table(outputs, "outputs")

@@ -64,3 +64,37 @@ def test_no_tokens_clear_the_gradient():
         assert mm.weight_grad(torch.zeros(0, rows, device=DEV, dtype=BF16), none, gain=gain, scale=-2.0, out=out) is out
         assert torch.equal(out.view(torch.int32), torch.zeros(rows, 64, device=DEV, dtype=torch.int32))
         assert bool((mm.weight_grad(torch.zeros(0, rows, device=DEV, dtype=BF16), none, gain=gain) == 0).all())
+
+
+class FetchedList:
+    """Gradients that are made on access and not kept."""
+
+    def __init__(self, tensors):
+        self.kept = tensors
+
+    def __len__(self):
+        return len(self.kept)
+
+    def __getitem__(self, k):
+        return self.kept[k].clone()
+
+
+def test_gradients_that_nobody_keeps():
+    """The norm's scratch memory and results are not allocated over gradients still to be read."""
+    print("[case] gradients that nobody keeps", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    for sizes in ([40], [130, 7, 4096], [2000] * 60, [3 << 20, 5, 1 << 20]):
+        ts = [torch.randn(s, generator=g, device=DEV).to(BF16 if k % 2 else F32) for k, s in enumerate(sizes)]
+        want = mm.grad_norm(ts, max_norm=0.5)
+        outs = [torch.empty_like(t) for t in ts]
+        mm.clip_grads(ts, 0.5, outputs=outs)
+        for _ in range(3):
+            for given in (FetchedList(ts), (t.clone() for t in ts)):
+                got = mm.grad_norm(given, max_norm=0.5)
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+            into = [torch.zeros_like(t) for t in ts]
+            total, coef = mm.clip_grads(FetchedList(ts), 0.5, outputs=into)
+            assert torch.equal(total, want[0]) and torch.equal(coef, want[1])
+            assert all(torch.equal(a, b) for a, b in zip(into, outs))
+            del got, into
